@@ -53,6 +53,14 @@ _lib.attn_fwd_ex.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f
 _lib.attn_bwd_ex.restype = _i
 _lib.attn_bwd_ex.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
                              _f, _i, _i, _i, _i, _vp, _sz, _vp]
+_lib.attn_fwd_sink.restype = _i
+_lib.attn_fwd_sink.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _i, _i, _i,
+                               _vp]
+_lib.attn_bwd_sink.restype = _i
+_lib.attn_bwd_sink.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                               _f, _i, _i, _i, _i, _i, _vp, _sz, _vp]
+_lib.attn_bwd_sink_workspace_bytes.restype = _sz
+_lib.attn_bwd_sink_workspace_bytes.argtypes = [_i] * 10
 _ll = ctypes.c_longlong
 _lib.attn_fwd_fp8.restype = _i
 _lib.attn_fwd_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _i, _f, _f,
@@ -138,6 +146,25 @@ def attn_bwd_ex(q, k, v, o, dO, lse, dq, dk, dv, B, H, Hkv, nq, nk, d, scale, wi
     return _lib.attn_bwd_ex(q, k, v, o, dO, lse, dq, dk, dv, B, H, Hkv, nq, nk, d, scale,
                             window_left, window_right, dtype, deterministic, workspace, ws_bytes,
                             stream)
+
+
+def attn_fwd_sink(q, k, v, o, lse, B, H, Hkv, nq, nk, d, scale, window_left, window_right, n_sink,
+                  dtype, stream) -> int:
+    return _lib.attn_fwd_sink(q, k, v, o, lse, B, H, Hkv, nq, nk, d, scale, window_left,
+                              window_right, n_sink, dtype, stream)
+
+
+def attn_bwd_sink(q, k, v, o, dO, lse, dq, dk, dv, B, H, Hkv, nq, nk, d, scale, window_left,
+                  window_right, n_sink, dtype, deterministic, workspace, ws_bytes, stream) -> int:
+    return _lib.attn_bwd_sink(q, k, v, o, dO, lse, dq, dk, dv, B, H, Hkv, nq, nk, d, scale,
+                              window_left, window_right, n_sink, dtype, deterministic, workspace,
+                              ws_bytes, stream)
+
+
+def attn_bwd_sink_workspace_bytes(B, H, Hkv, nq, nk, d, window_left, window_right, n_sink,
+                                  deterministic) -> int:
+    return _lib.attn_bwd_sink_workspace_bytes(B, H, Hkv, nq, nk, d, window_left, window_right,
+                                              n_sink, deterministic)
 
 
 def attn_fwd_fp8(q, k, v, o, lse, B, H, Hkv, nq, nk, d, scale, window_left, window_right,
@@ -336,16 +363,26 @@ def _window(causal, window):
     return wl, wr
 
 
-def forward(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, window=None):
+def _sinks(sinks):
+    n = int(sinks)
+    if n != sinks or n < 0 or n > 0x7fffffff:
+        raise ValueError("sinks must be a whole number of keys, 0 or more")
+    return n
+
+
+def forward(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, window=None,
+            sinks=0):
     """O, LSE = attention(q, k, v). q: contiguous CUDA tensor (B,H,n,d) or (n,d), bf16 or fp32;
     k, v: same shape, or (B,Hkv,nk,d) for grouped-query attention and / or another key length
     (cross-attention). window=(left, right): key j visible to query i iff
-    i+nk-nq-left <= j <= i+nk-nq+right (negative = unbounded); causal=True is (-1, 0).
+    i+nk-nq-left <= j <= i+nk-nq+right (negative = unbounded); causal=True is (-1, 0). The first
+    `sinks` keys stay visible beyond the window's left bound (never its right one).
     Returns O (same dtype/shape as q) and LSE (fp32, (B,H,nq)); a query that sees no key gets
     O = 0 and LSE = -inf."""
     import torch
     B, H, n, d = _dims(q)
     Hkv, nk = _kv_heads(q, k, v)
+    sinks = _sinks(sinks)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
@@ -355,7 +392,11 @@ def forward(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, 
     _packed("forward", q, k, v, out, lse)
     _shaped("forward", [(out, q.shape, q.dtype), (lse, (B, H, n) if q.dim() == 4 else (n,),
                                                   torch.float32)])
-    if nk != n or window is not None:
+    if sinks:
+        wl, wr = _window(causal, window)
+        rc = attn_fwd_sink(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, Hkv, n, nk, d,
+                           float(scale), wl, wr, sinks, _dtype_code(q), _stream_handle(stream))
+    elif nk != n or window is not None:
         wl, wr = _window(causal, window)
         rc = attn_fwd_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, Hkv, n, nk, d,
                          float(scale), wl, wr, _dtype_code(q), _stream_handle(stream))
@@ -391,9 +432,9 @@ def forward_accumulate(q, k, v, o_acc, lse_acc, first=False, causal=False, scale
 
 
 def backward(q, k, v, o, do, lse, causal=False, scale=None, deterministic=False, dq=None,
-             dk=None, dv=None, workspace=None, stream=None, window=None):
+             dk=None, dv=None, workspace=None, stream=None, window=None, sinks=0):
     """dQ, dK, dV of attention given dO (bf16 tensors, lse from `forward` with the same causal /
-    window arguments). dK, dV have k's (B, Hkv, nk, d) shape and, for grouped-query inputs, sum
+    window / sinks arguments). dK, dV have k's (B, Hkv, nk, d) shape and, for grouped-query inputs, sum
     over each group's query heads."""
     import torch
     B, H, n, d = _dims(q)
@@ -403,7 +444,13 @@ def backward(q, k, v, o, do, lse, causal=False, scale=None, deterministic=False,
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    need = attn_bwd_workspace_bytes(B, H, n, d, int(bool(deterministic)))
+    sinks = _sinks(sinks)
+    if sinks:
+        wl, wr = _window(causal, window)
+        need = attn_bwd_sink_workspace_bytes(B, H, Hkv, n, nk, d, wl, wr, sinks,
+                                             int(bool(deterministic)))
+    else:
+        need = attn_bwd_workspace_bytes(B, H, n, d, int(bool(deterministic)))
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _packed("backward", q, k, v, o, do, lse, dq, dk, dv, workspace)
@@ -412,7 +459,12 @@ def backward(q, k, v, o, do, lse, causal=False, scale=None, deterministic=False,
                          (lse, lse_shape, torch.float32), (dq, q.shape, q.dtype),
                          (dk, k.shape, k.dtype), (dv, v.shape, v.dtype)])
     ws_bytes = workspace.numel() * workspace.element_size()
-    if nk != n or window is not None:
+    if sinks:
+        rc = attn_bwd_sink(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
+                           _ptr(dk), _ptr(dv), B, H, Hkv, n, nk, d, float(scale), wl, wr, sinks,
+                           _dtype_code(q), int(bool(deterministic)), _ptr(workspace), ws_bytes,
+                           _stream_handle(stream))
+    elif nk != n or window is not None:
         wl, wr = _window(causal, window)
         rc = attn_bwd_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
                          _ptr(dk), _ptr(dv), B, H, Hkv, n, nk, d, float(scale), wl, wr,

@@ -173,9 +173,14 @@ unsigned attn_set_wait_timeout_us(unsigned us) {
     return g_timeout_us.exchange(us);
 }
 
+// Sinks that change the mask: none when the left bound is open, at most every key.
+static int sinks_in_use(int n_sink, int wl, int nk) {
+    return wl < 0 ? 0 : (n_sink < nk ? n_sink : nk);
+}
+
 static int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                     int H, int Hkv, int nq, int nk, int d, float scale, int wl, int wr, int dtype,
-                    void* stream) {
+                    void* stream, int n_sink = 0) {
     if (!q || !k || !v || !o || !lse) return ATTN_ERR_INVALID;
     int rc = validate_common(B, H, nq, d, scale, dtype);
     if (rc) return rc;
@@ -189,6 +194,7 @@ static int fwd_impl(const void* q, const void* k, const void* v, void* o, float*
     a.scale = scale;
     a.wl = wl < 0 ? -1 : wl;
     a.wr = wr < 0 ? -1 : wr;
+    a.ns = sinks_in_use(n_sink, wl, nk);
     a.q_descale = a.k_descale = a.v_descale = 1.f;
     a.timeout_ns = static_cast<uint64_t>(g_timeout_us.load()) * 1000ull;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -212,6 +218,14 @@ int attn_fwd_ex(const void* q, const void* k, const void* v, void* o, float* lse
                 int dtype, void* stream) {
     return fwd_impl(q, k, v, o, lse, B, H, Hkv, nq, nk, d, scale, window_left, window_right, dtype,
                     stream);
+}
+
+int attn_fwd_sink(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
+                  int Hkv, int nq, int nk, int d, float scale, int window_left, int window_right,
+                  int n_sink, int dtype, void* stream) {
+    if (n_sink < 0) return ATTN_ERR_INVALID;
+    return fwd_impl(q, k, v, o, lse, B, H, Hkv, nq, nk, d, scale, window_left, window_right, dtype,
+                    stream, n_sink);
 }
 
 int attn_fwd_accumulate(const void* q, const void* k, const void* v, float* o_acc, float* lse_acc,
@@ -273,17 +287,40 @@ size_t attn_bwd_workspace_bytes(int B, int H, int n, int d, int deterministic) {
     return ws_layout(B, H, n, d, deterministic).total;
 }
 
+// fp32 dK and dV partials of the key tiles that hold a sink (see BwdArgs::sink_buf).
+static size_t sink_buf_bytes(int B, int H, int Hkv, int nq, int nk, int d, int wl, int wr, int ns) {
+    const size_t tiles = (static_cast<size_t>(ns) + 127) / 128;
+    return 2 * static_cast<size_t>(B) * Hkv * tiles * bwd_sink_parts(H, Hkv, nq, nk, d, wl, wr) * 128 *
+           d * sizeof(float);
+}
+
+size_t attn_bwd_sink_workspace_bytes(int B, int H, int Hkv, int nq, int nk, int d, int window_left,
+                                     int window_right, int n_sink, int deterministic) {
+    if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || nq < 1 || nk < 1 || d < 1 || n_sink < 0)
+        return 0;
+    const int ns = sinks_in_use(n_sink, window_left, nk);
+    return ws_layout(B, H, nq, d, deterministic).total +
+           (ns > 0 ? sink_buf_bytes(B, H, Hkv, nq, nk, d, window_left, window_right, ns) : 0);
+}
+
 static int bwd_impl(const void* q, const void* k, const void* v, const void* o, const void* dO,
                     const float* lse, void* dq, void* dk, void* dv, int B, int H, int Hkv, int nq,
                     int nk, int d, float scale, int wl, int wr, int dtype, int deterministic,
-                    void* workspace, size_t ws_bytes, void* stream) {
+                    void* workspace, size_t ws_bytes, void* stream, int n_sink = 0) {
     int rc = validate_bwd(q, k, v, o, dO, lse, dq, dk, dv, B, H, Hkv, nq, nk, d, scale, dtype);
     if (rc) return rc;
     WsLayout w = ws_layout(B, H, nq, d, deterministic);
+    const int ns = sinks_in_use(n_sink, wl, nk);
+    const size_t sink_bytes = ns > 0 ? sink_buf_bytes(B, H, Hkv, nq, nk, d, wl, wr, ns) : 0;
     if (!workspace) return ATTN_ERR_INVALID;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_INVALID;
-    if (ws_bytes < w.total) return ATTN_ERR_WORKSPACE;
+    if (ws_bytes < w.total + sink_bytes) return ATTN_ERR_WORKSPACE;
     BwdArgs a;
+    if (ns > 0) {
+        a.ns = ns;
+        a.sink_parts = bwd_sink_parts(H, Hkv, nq, nk, d, wl, wr);
+        a.sink_buf = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.total);
+    }
     a.q = q; a.k = k; a.v = v; a.o = o; a.dO = dO; a.lse = lse;
     a.dq = dq; a.dk = dk; a.dv = dv;
     a.B = B; a.H = H; a.nq = nq; a.nk = nk; a.d = d; a.Hkv = Hkv;
@@ -323,6 +360,15 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
                 int deterministic, void* workspace, size_t ws_bytes, void* stream) {
     return bwd_impl(q, k, v, o, dO, lse, dq, dk, dv, B, H, Hkv, nq, nk, d, scale, window_left,
                     window_right, dtype, deterministic, workspace, ws_bytes, stream);
+}
+
+int attn_bwd_sink(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                  const float* lse, void* dq, void* dk, void* dv, int B, int H, int Hkv, int nq,
+                  int nk, int d, float scale, int window_left, int window_right, int n_sink,
+                  int dtype, int deterministic, void* workspace, size_t ws_bytes, void* stream) {
+    if (n_sink < 0) return ATTN_ERR_INVALID;
+    return bwd_impl(q, k, v, o, dO, lse, dq, dk, dv, B, H, Hkv, nq, nk, d, scale, window_left,
+                    window_right, dtype, deterministic, workspace, ws_bytes, stream, n_sink);
 }
 
 // Workspace arguments shared by the backward entry points: present, 256-byte aligned, large

@@ -24,6 +24,11 @@
 // Masks (causal, sliding window, query/key lengths that differ; see MaskSpec): key tile j only
 // meets the query tiles that hold a query which sees one of its keys; a key tile that no query
 // sees gets dK = dV = 0.
+// Sinks (MaskSpec::ns, the SINK kernels): a key tile that holds a sink meets every later query tile,
+// nq/(window + 128) times the work of the others, and would run on alone at the end. Its query
+// tiles are shared by sink_parts CTAs, each about as long as a window tile's; every one stores its dK,
+// dV partial in fp32, and bwd_sink_sum adds the parts in a fixed order. dQ needs nothing of its own:
+// the partial of a (query tile, key tile) pair still comes from exactly one CTA.
 #include "kernels.h"
 #include "sm100_ptx.cuh"
 
@@ -76,12 +81,47 @@ struct BwdKParams {
 
 // Accumulating launches (the backward in parts) add dK and dV in fp32 into these arrays
 // (B, Hkv, nk, d) instead of storing them; a kernel parameter of its own, used only by the
-// accumulating instantiation of each main kernel.
+// accumulating instantiation of each main kernel. The SINK instantiations store the partials of the
+// sinks' key tiles there.
 struct AccOut {
     float* dk;
     float* dv;
     long long rows;   // rows between consecutive K/V heads of dk, dv
+    int sink_nt, sink_parts;   // SINK: key tiles that hold a sink, CTAs for each
 };
+
+// Key tile and part (CTA among those of a sink tile; 0 otherwise) of a head's CTA number `idx`. Sink
+// tiles go first; in the deterministic mode key tiles go from the last to the first, so that a
+// CTA only ever waits for CTAs launched before it.
+__device__ __forceinline__ void sink_cta(const BwdKParams& p, const AccOut& a, int idx, int& j,
+                                         int& part) {
+    const int sinks = a.sink_nt * a.sink_parts;
+    if (p.deterministic) idx = sinks + p.nkt - a.sink_nt - 1 - idx;
+    const bool sink = idx < sinks;
+    j = sink ? idx / a.sink_parts : a.sink_nt + idx - sinks;
+    part = sink ? idx % a.sink_parts : 0;
+}
+
+// First of a sink tile's `total` steps that its CTA `part` takes.
+__device__ __forceinline__ int sink_share(const AccOut& a, int part, int total) {
+    return static_cast<int>(static_cast<long long>(total) * part / a.sink_parts);
+}
+
+// Rows of a sink tile's partial sums (fp32, 128 x D) of part `part`.
+template <int D>
+__device__ __forceinline__ size_t sink_rows(const AccOut& a, int kvbh, int j, int part) {
+    return ((static_cast<size_t>(kvbh) * a.sink_nt + j) * a.sink_parts + part) * 128 * D;
+}
+
+// dst[0 .. N) = mul · (TMEM words u as fp32); dst 16-byte aligned.
+template <int N>
+__device__ __forceinline__ void store_row_f32(float* dst, const uint32_t* u, float mul) {
+#pragma unroll
+    for (int c = 0; c < N / 4; ++c)
+        reinterpret_cast<float4*>(dst)[c] =
+            make_float4(__uint_as_float(u[4 * c]) * mul, __uint_as_float(u[4 * c + 1]) * mul,
+                        __uint_as_float(u[4 * c + 2]) * mul, __uint_as_float(u[4 * c + 3]) * mul);
+}
 
 // dst[0 .. N) += mul · (TMEM words u as fp32); dst 16-byte aligned. Vector reductions performed
 // in L2: nothing waits for them, and each element of dst gets one addition per launch (one CTA
@@ -197,6 +237,38 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_kernel(const float* __rest
 }
 
 // ------------------------------------------------------------------------------------------
+// dK, dV of the key tiles that hold a sink: the sum of their parts in order, rounded to bf16.
+// One thread per 4 channels of a key row and of dK or dV; the parts of a row lie 128·D floats apart.
+// ------------------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const float* __restrict__ part,
+                                                           __nv_bfloat16* __restrict__ dk,
+                                                           __nv_bfloat16* __restrict__ dv, int nk,
+                                                           int nt, int parts, int rows,
+                                                           long long items, size_t dv_off) {
+    constexpr int G = D / 4;
+    for (long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; t < items;
+         t += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const int g = static_cast<int>(t % G);
+        const long long r = t / G;                    // (K/V head, dK or dV, key row)
+        const int key = static_cast<int>(r % rows);
+        const int which = static_cast<int>(r / rows % 2);
+        const long long kvbh = r / rows / 2;
+        const float* src = part + (which ? dv_off : 0) +
+                           (static_cast<size_t>(kvbh * nt + key / 128) * parts * 128 + key % 128) * D +
+                           g * 4;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int x = 0; x < parts; ++x) {
+            const float4 b = *reinterpret_cast<const float4*>(src + static_cast<size_t>(x) * 128 * D);
+            a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+        }
+        *reinterpret_cast<uint2*>((which ? dv : dk) + (static_cast<size_t>(kvbh) * nk + key) * D + g * 4) =
+            make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    }
+}
+
+// ------------------------------------------------------------------------------------------
 // Main backward kernel.
 //
 // Roles (320 threads): warps 0-3 = compute warpgroup 0 (query columns 0-63 of each tile),
@@ -210,7 +282,7 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_kernel(const float* __rest
 // softmax of the next overlap the dK/dQ MMAs. dQ has TMEM lane = query, and each thread adds
 // 16-byte pieces of its row to the fp32 accumulator with red.global.
 // ------------------------------------------------------------------------------------------
-template <int D, bool ACC>
+template <int D, bool ACC, bool SINK = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -234,20 +306,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // Heads in groups of p.group (a group's Q, dO, K, V and dQ rows stay in L2); within a group,
     // key tiles go from small j (most causal work) to large j across the group's heads.
     const int L = blockIdx.x;
-    const int gbase = (L / (p.group * p.nkt)) * p.group;
+    const int per_head = SINK ? p.nkt + acc.sink_nt * (acc.sink_parts - 1) : p.nkt;   // CTAs
+    const int gbase = (L / (p.group * per_head)) * p.group;
     const int gsize = min(p.group, p.BH - gbase);
-    const int r_in = L - gbase * p.nkt;
+    const int r_in = L - gbase * per_head;
     // deterministic mode adds dQ partials in decreasing key-tile order, so CTAs of high key tiles
     // are launched first (a CTA only ever waits for CTAs launched before it)
-    const int j = p.deterministic ? p.nkt - 1 - r_in / gsize : r_in / gsize;
+    int sink_j = 0, part = 0;
+    if constexpr (SINK) sink_cta(p, acc, r_in / gsize, sink_j, part);
+    const int j = SINK ? sink_j : p.deterministic ? p.nkt - 1 - r_in / gsize : r_in / gsize;
     const int kvbh = gbase + r_in % gsize;        // K/V head of this CTA
     const MaskSpec& mk = p.mask;
     const int nk = mk.nk;
     const int qt128 = p.n_pad / 128;              // semaphore stride per query head
     int i_begin, i_end;                           // query tiles that meet this key tile
-    visible_query_tiles(mk, j * 128LL, min(j * 128LL + 127, nk - 1LL), 128, i_begin, i_end);
+    if constexpr (SINK)
+        query_tiles_of_key_tile(mk, j, 128, 128, i_begin, i_end);
+    else
+        visible_query_tiles(mk, j * 128LL, min(j * 128LL + 127, nk - 1LL), 128, i_begin, i_end);
     const int NT = i_end - i_begin;               // query tiles per query head
-    const int NTT = NT * p.kv_group;              // over all query heads sharing this K/V head
+    // steps of this CTA: all query heads sharing this K/V head, or a part of them for a sink tile
+    const bool sink = SINK && j < acc.sink_nt;
+    const int it0 = SINK && sink ? sink_share(acc, part, NT * p.kv_group) : 0;
+    const int NTT = SINK && sink ? sink_share(acc, part + 1, NT * p.kv_group) - it0 : NT * p.kv_group;
 
     if (threadIdx.x == 0) {
         mbar_init(&bars->kv_full, 1);
@@ -297,8 +378,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int it = 0; it < NTT; ++it) {
                 const int st = it & 1, f = it >> 1;
                 if (f > 0 && !bounded_wait(&bars->q_empty[st], (f - 1) & 1, abort, lim)) break;
-                const int i = i_begin + it % NT;
-                const int qbh = kvbh * p.kv_group + it / NT;
+                const int i = i_begin + (it0 + it) % NT;
+                const int qbh = kvbh * p.kv_group + (it0 + it) / NT;
                 mbar_arrive_expect_tx(&bars->q_full[st], 2 * C::TILE);
                 for (int ch = 0; ch < C::NCH; ++ch) {
                     tma_load_3d(sQ + st * C::TILE + ch * C::CHUNK, &tmQ, &bars->q_full[st],
@@ -456,7 +537,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         int qmin = 1, qmax = 0;
         if (kidx < nk) {
             qmin = mk.wr < 0 ? -0x7fffffff : clamp_int(kidx - mk.off - mk.wr);
-            qmax = mk.wl < 0 ? 0x7fffffff : clamp_int(kidx - mk.off + mk.wl);
+            qmax = mk.wl < 0 || (SINK && kidx < mk.ns) ? 0x7fffffff
+                                                       : clamp_int(kidx - mk.off + mk.wl);
         }
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_base + COL_S;
@@ -476,8 +558,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
         // dQ partial of tile `it` out of TMEM into the fp32 accumulator
         auto drain = [&](int it) -> bool {
-            const int i = i_begin + it % NT;
-            const int qbh = kvbh * p.kv_group + it / NT;
+            const int i = i_begin + (it0 + it) % NT;
+            const int qbh = kvbh * p.kv_group + (it0 + it) / NT;
             const int b2 = it & 1;
             if (!wait_all(&bars->dq_full[b2], (it >> 1) & 1)) return false;
             tc_fence_after();
@@ -485,7 +567,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 // add this tile's partial only after every higher key tile that meets the query
                 // tile has added its own (each CTA contributes two halves, one per warpgroup)
                 volatile int* sem = p.sems + static_cast<size_t>(qbh) * qt128 + i;
-                const int need = 2 * (last_key_tile(mk, i * 128LL, 128, 128) - j);
+                const int need = 2 * (SINK ? key_tiles_above(mk, i * 128LL, 128, 128, j)
+                                           : last_key_tile(mk, i * 128LL, 128, 128) - j);
                 bool got = true;
                 if (t == 0) {
                     const uint64_t t0 = globaltimer_ns();
@@ -544,8 +627,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         };
 
         for (int it = 0; it < NTT; ++it) {
-            const int i = i_begin + it % NT;
-            const int qbh = kvbh * p.kv_group + it / NT;
+            const int i = i_begin + (it0 + it) % NT;
+            const int qbh = kvbh * p.kv_group + (it0 + it) / NT;
             float* sL = sStat + (g * 2 + (it & 1)) * 128;
             float* sD = sL + 64;
             {
@@ -566,7 +649,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             {   // every key of the tile visible to every query of the tile: no mask needed
                 long long flo, fhi;
                 visible_keys(mk, i * 128LL + 127, i * 128LL, flo, fhi);
-                edge = !(flo <= j * 128LL && j * 128LL + 127 <= fhi);
+                edge = !((flo <= j * 128LL || (SINK && j * 128LL + 128 <= mk.ns)) &&
+                         j * 128LL + 127 <= fhi);
             }
             const int q0 = i * 128 + cb;
 #pragma unroll
@@ -625,7 +709,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (ok && NTT > 0) ok = drain(NTT - 1);
         if (ok && NTT == 0) {
             // no query sees these keys: dK = dV = 0
-            if (kidx < nk && !ACC) {     // (accumulating: nothing to add)
+            if (SINK && sink) {
+                const size_t row = sink_rows<D>(acc, kvbh, j, part) + r * D + g * (D / 2);
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x) {
+                    reinterpret_cast<float4*>(acc.dk + row)[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    reinterpret_cast<float4*>(acc.dv + row)[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            } else if (kidx < nk && !ACC) {     // (accumulating: nothing to add)
                 const size_t orow = (static_cast<size_t>(kvbh) * nk + kidx) * D + g * (D / 2);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
@@ -655,6 +746,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                                 (static_cast<size_t>(kvbh) * acc.rows + kidx) * D +
                                                 g * (D / 2) + cc,
                                             u, mul);
+                    } else if (SINK && sink) {
+                        store_row_f32<16>((which == 0 ? acc.dv : acc.dk) +
+                                              sink_rows<D>(acc, kvbh, j, part) + r * D + g * (D / 2) + cc,
+                                          u, mul);
                     } else {
                         uint32_t w[8];
 #pragma unroll
@@ -753,7 +848,7 @@ struct Bars {
 static_assert(sizeof(Bars) <= 256, "barrier block");
 }  // namespace q64
 
-template <bool ACC>
+template <bool ACC, bool SINK = false>
 __global__ void __launch_bounds__(q64::kThreads, 1)
     bwd_main_q64_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -779,19 +874,28 @@ __global__ void __launch_bounds__(q64::kThreads, 1)
     const int lane = threadIdx.x & 31;
     // Heads in groups of p.group (see bwd_main_kernel); key tiles of 128 keys, small j first.
     const int L = blockIdx.x;
-    const int gbase = (L / (p.group * p.nkt)) * p.group;
+    const int per_head = SINK ? p.nkt + acc.sink_nt * (acc.sink_parts - 1) : p.nkt;   // CTAs
+    const int gbase = (L / (p.group * per_head)) * p.group;
     const int gsize = min(p.group, p.BH - gbase);
-    const int r_in = L - gbase * p.nkt;
+    const int r_in = L - gbase * per_head;
     // deterministic mode: high key tiles first (see bwd_main_kernel)
-    const int j = p.deterministic ? p.nkt - 1 - r_in / gsize : r_in / gsize;
+    int sink_j = 0, part = 0;
+    if constexpr (SINK) sink_cta(p, acc, r_in / gsize, sink_j, part);
+    const int j = SINK ? sink_j : p.deterministic ? p.nkt - 1 - r_in / gsize : r_in / gsize;
     const int kvbh = gbase + r_in % gsize;         // K/V head of this CTA
     const MaskSpec& mk = p.mask;
     const int nk = mk.nk;
     const int qt64 = p.n_pad / BQ;                 // 64-row query tiles per query head
     int i_begin, i_end;                            // 64-row query tiles that meet this key tile
-    visible_query_tiles(mk, j * 128LL, min(j * 128LL + 127, nk - 1LL), BQ, i_begin, i_end);
-    const int NT = i_end - i_begin;                // query tiles per query head
-    const int NTT = NT * p.kv_group;               // over all query heads sharing this K/V head
+    if constexpr (SINK)
+        query_tiles_of_key_tile(mk, j, 128, BQ, i_begin, i_end);
+    else
+        visible_query_tiles(mk, j * 128LL, min(j * 128LL + 127, nk - 1LL), BQ, i_begin, i_end);
+    const int NT = i_end - i_begin;               // query tiles per query head
+    // steps of this CTA: all query heads sharing this K/V head, or a part of them for a sink tile
+    const bool sink = SINK && j < acc.sink_nt;
+    const int it0 = SINK && sink ? sink_share(acc, part, NT * p.kv_group) : 0;
+    const int NTT = SINK && sink ? sink_share(acc, part + 1, NT * p.kv_group) - it0 : NT * p.kv_group;
 
     if (threadIdx.x == 0) {
         mbar_init(&bars->kv_full, 1);
@@ -844,8 +948,8 @@ __global__ void __launch_bounds__(q64::kThreads, 1)
             for (int it = 0; it < NTT; ++it) {
                 const int st = it % STAGES, f = it / STAGES;
                 if (f > 0 && !bounded_wait(&bars->q_empty[st], (f - 1) & 1, abort, lim)) break;
-                const int i = i_begin + it % NT;
-                const int bh = kvbh * p.kv_group + it / NT;   // query head
+                const int i = i_begin + (it0 + it) % NT;
+                const int bh = kvbh * p.kv_group + (it0 + it) / NT;   // query head
                 mbar_arrive_expect_tx(&bars->q_full[st], 2 * QTILE + 2 * 256);
                 for (int ch = 0; ch < 2; ++ch) {
                     tma_load_3d(sQ + st * QTILE + ch * QCHUNK, &tmQ, &bars->q_full[st], ch * 64,
@@ -981,8 +1085,8 @@ __global__ void __launch_bounds__(q64::kThreads, 1)
             reg_fence<64>(u);
             tc_fence_before();
             mbar_arrive(&bars->dq_drained[x]);
-            const int i = i_begin + it % NT;
-            const int qbh = kvbh * p.kv_group + it / NT;
+            const int i = i_begin + (it0 + it) % NT;
+            const int qbh = kvbh * p.kv_group + (it0 + it) / NT;
             const int row0 = qbh * p.n_pad + i * BQ;       // accumulator row of the tile's query 0
             volatile int* sem = p.deterministic
                                     ? p.sems + (static_cast<size_t>(qbh) * qt64 + i) * 4 + w
@@ -1001,7 +1105,9 @@ __global__ void __launch_bounds__(q64::kThreads, 1)
                     bool got = true;
                     if (h == 0 && sem) {
                         // the key tiles above this one that meet query tile i add first
-                        const int need = last_key_tile(mk, static_cast<long long>(i) * BQ, BQ, 128) - j;
+                        const int need =
+                            SINK ? key_tiles_above(mk, static_cast<long long>(i) * BQ, BQ, 128, j)
+                                 : last_key_tile(mk, static_cast<long long>(i) * BQ, BQ, 128) - j;
                         const uint64_t t0 = globaltimer_ns();
                         while (ld_acquire_gpu(sem) < need) {   // the acquire orders the adds below
                             if (*abort || globaltimer_ns() - t0 > lim) {
@@ -1047,7 +1153,8 @@ __global__ void __launch_bounds__(q64::kThreads, 1)
         int qmin = 1, qmax = 0;
         if (kidx < nk) {
             qmin = mk.wr < 0 ? -0x7fffffff : clamp_int(kidx - mk.off - mk.wr);
-            qmax = mk.wl < 0 ? 0x7fffffff : clamp_int(kidx - mk.off + mk.wl);
+            qmax = mk.wl < 0 || (SINK && kidx < mk.ns) ? 0x7fffffff
+                                                       : clamp_int(kidx - mk.off + mk.wl);
         }
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_base + COL_S + 64 * x;
@@ -1061,7 +1168,7 @@ __global__ void __launch_bounds__(q64::kThreads, 1)
         bool ok = true;
 
         for (int it = x; it < NTT; it += 2) {
-            const int i = i_begin + it % NT;
+            const int i = i_begin + (it0 + it) % NT;
             const int st = it % STAGES;
             const uint32_t ph = static_cast<uint32_t>((it >> 1) & 1);
             const float* L2 = sL2 + st * 64;
@@ -1074,7 +1181,8 @@ __global__ void __launch_bounds__(q64::kThreads, 1)
                 long long flo, fhi;
                 visible_keys(mk, static_cast<long long>(i) * BQ + BQ - 1,
                              static_cast<long long>(i) * BQ, flo, fhi);
-                edge = !(flo <= j * 128LL && j * 128LL + 127 <= fhi);
+                edge = !((flo <= j * 128LL || (SINK && j * 128LL + 128 <= mk.ns)) &&
+                         j * 128LL + 127 <= fhi);
             }
             {   // the whole S^T row of the tile (64 columns): two loads, one wait
                 uint32_t u[64];
@@ -1141,7 +1249,14 @@ __global__ void __launch_bounds__(q64::kThreads, 1)
         // ---- epilogue: warpgroup x writes head-dim columns 64x .. 64x+63 of dV and dK
         if (ok && NTT == 0) {
             // no query sees these keys: dK = dV = 0
-            if (kidx < nk && !ACC) {     // (accumulating: nothing to add)
+            if (SINK && sink) {
+                const size_t row = sink_rows<D>(acc, kvbh, j, part) + r * D + x * 64;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    reinterpret_cast<float4*>(acc.dk + row)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    reinterpret_cast<float4*>(acc.dv + row)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            } else if (kidx < nk && !ACC) {     // (accumulating: nothing to add)
                 const size_t orow = (static_cast<size_t>(kvbh) * nk + kidx) * D + x * 64;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -1172,6 +1287,10 @@ __global__ void __launch_bounds__(q64::kThreads, 1)
                                                 (static_cast<size_t>(kvbh) * acc.rows + kidx) * D +
                                                 x * 64 + cc,
                                             u, mul);
+                    } else if (SINK && sink) {
+                        store_row_f32<32>((which == 0 ? acc.dv : acc.dk) +
+                                              sink_rows<D>(acc, kvbh, j, part) + r * D + x * 64 + cc,
+                                          u, mul);
                     } else {
                         uint32_t w[16];
 #pragma unroll
@@ -1240,7 +1359,7 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
             const size_t n_sems = static_cast<size_t>(BH) * (n_pad / 64) * 4;
             if ((e = cudaMemsetAsync(a.sems, 0, n_sems * sizeof(int), stream)) != cudaSuccess) return e;
         }
-        const AccOut acc{a.dk_acc32, a.dv_acc32, a.kv_rows > 0 ? a.kv_rows : a.nk};
+        AccOut acc{a.dk_acc32, a.dv_acc32, a.kv_rows > 0 ? a.kv_rows : a.nk, 0, 1};
         BwdKParams kp;
         kp.lse = a.lse;
         // the workspace rows of this launch's first query, in every head
@@ -1258,11 +1377,18 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
         kp.kv_group = kvg;
         kp.deterministic = a.deterministic;
         kp.group = group;
-        kp.mask = MaskSpec{a.nq, a.nk, a.wl, a.wr, static_cast<long long>(a.nk) - a.nq};
+        kp.mask = MaskSpec{a.nq, a.nk, a.wl, a.wr, static_cast<long long>(a.nk) - a.nq, a.ns};
+        size_t sink_half = 0;          // floats of all dK partials
+        if (a.ns > 0) {
+            const int nt = sink_tiles(kp.mask, 128);
+            sink_half = static_cast<size_t>(BHkv) * nt * a.sink_parts * 128 * D;
+            acc = AccOut{a.sink_buf, a.sink_buf + sink_half, 0, nt, a.sink_parts};
+        }
         kp.scale = a.scale;
         kp.scale_log2 = a.scale * kBwdLog2e;
         kp.timeout_ns = a.timeout_ns;
-        const long long grid = static_cast<long long>(nkt) * BHkv;
+        const long long grid =
+            (nkt + static_cast<long long>(acc.sink_nt) * (acc.sink_parts - 1)) * BHkv;
         if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
         const int qbox = D == 128 ? q64::BQ : 128;
         CUtensorMap mq, mk, mv, mdo;
@@ -1275,14 +1401,16 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
             if ((e = make_tmap_acc(&macc, kp.dq_acc,
                                    static_cast<long long>(BH) * n_pad - a.q_row0, D)) != cudaSuccess)
                 return e;
-            const auto kern = acc.dk ? bwd_main_q64_kernel<true> : bwd_main_q64_kernel<false>;
+            const auto kern = a.ns > 0 ? bwd_main_q64_kernel<false, true>
+                              : acc.dk ? bwd_main_q64_kernel<true> : bwd_main_q64_kernel<false>;
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, q64::SMEM);
             if (e != cudaSuccess) return e;
             if (ev && ev[1] && (e = cudaEventRecord(ev[1], stream)) != cudaSuccess) return e;
             kern<<<static_cast<unsigned>(grid), q64::kThreads, q64::SMEM, stream>>>(
                 mq, mk, mv, mdo, macc, kp, acc);
         } else {
-            const auto kern = acc.dk ? bwd_main_kernel<D, true> : bwd_main_kernel<D, false>;
+            const auto kern = a.ns > 0 ? bwd_main_kernel<D, false, true>
+                              : acc.dk ? bwd_main_kernel<D, true> : bwd_main_kernel<D, false>;
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
             if (e != cudaSuccess) return e;
             if (ev && ev[1] && (e = cudaEventRecord(ev[1], stream)) != cudaSuccess) return e;
@@ -1290,6 +1418,16 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
                                                                                 acc);
         }
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (a.ns > 0) {
+            const long long rows = static_cast<long long>(acc.sink_nt) * 128;
+            const int live = static_cast<int>(rows < a.nk ? rows : a.nk);
+            const long long items = static_cast<long long>(BHkv) * 2 * live * (D / 4);
+            long long blocks = (items + 255) / 256;
+            if (blocks > 148 * 16) blocks = 148 * 16;
+            bwd_sink_sum_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+                a.sink_buf, kp.dk, kp.dv, a.nk, acc.sink_nt, acc.sink_parts, live, items, sink_half);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        }
         if (ev && ev[2] && (e = cudaEventRecord(ev[2], stream)) != cudaSuccess) return e;
     }
     // 3. dQ convert
@@ -1306,6 +1444,18 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+int bwd_sink_parts(int H, int Hkv, int nq, int nk, int d, int wl, int wr) {
+    const int bq = d == 128 ? q64::BQ : 128;
+    const long long kvg = H / Hkv;
+    const long long all = ((static_cast<long long>(nq) + bq - 1) / bq) * kvg;
+    // query tiles that a key tile of the window meets; an unbounded right side: half of all
+    const long long span = wr < 0 ? nq / 2 : static_cast<long long>(wl) + wr + 128;
+    long long each = (span / bq + 1) * kvg;
+    if (each < 8) each = 8;
+    const long long parts = (all + each - 1) / each;
+    return static_cast<int>(parts < 1 ? 1 : (parts > 256 ? 256 : parts));
+}
 
 cudaError_t launch_bwd_bf16(const BwdArgs& a, cudaStream_t stream) {
     switch (a.d) {

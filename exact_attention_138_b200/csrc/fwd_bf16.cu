@@ -29,6 +29,9 @@
 //   Masks (causal, sliding window, query/key lengths that differ; see MaskSpec): each query tile
 //   visits only the key tiles that hold a key it can see; the two tiles of a pair stream the
 //   union of their ranges once. A row that sees no key gets O = 0 and LSE = -inf.
+//   Sinks (MaskSpec::ns, the SINK kernels): a pair whose windows begin behind the sinks streams the
+//   key tiles that hold them first, then the windows' union; a pair whose window begins at or
+//   next to a sink tile streams one range from key 0. Only tiles that straddle a boundary are masked.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -134,7 +137,8 @@ __device__ __forceinline__ void store_p(uint32_t* u, int c, float p0, float p1) 
 // ACC: p.o and p.lse are a running fp32 result (o_acc, and lse_acc in natural log) over earlier
 // key sets, into which this launch folds its own (acc_first: initialised instead of read); their
 // heads start acc_rows rows apart.
-template <int D, bool F8, bool SPLIT, bool ACC = false>
+// SINK: the first mask.ns keys stay visible (see above).
+template <int D, bool F8, bool SPLIT, bool ACC = false, bool SINK = false>
 __device__ __forceinline__ void fwd_body(const CUtensorMap* tmQ_, const CUtensorMap* tmK_,
                                          const CUtensorMap* tmV_, const FwdKParams& p,
                                          int acc_first = 0, long long acc_rows = 0) {
@@ -179,20 +183,55 @@ __device__ __forceinline__ void fwd_body(const CUtensorMap* tmQ_, const CUtensor
             }
         }
     }
+    // key tiles [SB, SB + SU) of the sinks come first in the pair's stream; S0, S1 = SU, or 0 for a
+    // query tile that sees nothing (J0, T stay those of the window's range)
+    int SB = 0, SU = 0, S0 = 0, S1 = 0;
+    if constexpr (SINK) {
+        const int NS = sink_tiles(mk, C::BN);
+        const bool joined = (T[0] > 0 && J0[0] <= NS) || (T[1] > 0 && J0[1] <= NS);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+            if (T[g] > 0) {
+                if (joined) {        // windows of a pair begin at most one tile apart
+                    T[g] += J0[g];
+                    J0[g] = 0;
+                } else {
+                    SU = NS;
+                    (g == 0 ? S0 : S1) = NS;
+                }
+            }
+    }
     if constexpr (SPLIT) {
         // this CTA's share (its rank in the cluster) of each tile's key tiles
         const int rank = static_cast<int>(blockIdx.x) % p.split;
+        if constexpr (SINK) {
+            SB = SU * rank / p.split;
+            SU = SU * (rank + 1) / p.split - SB;
+        }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             const int a0 = T[g] * rank / p.split, a1 = T[g] * (rank + 1) / p.split;
             J0[g] += a0;
             T[g] = a1 - a0;
         }
+        if constexpr (SINK) {
+            S0 = min(S0, SU);
+            S1 = min(S1, SU);
+        }
     }
+    auto sinks_of = [&](int g) -> int {
+        if constexpr (SINK) return g == 0 ? S0 : S1;
+        return 0;
+    };
     const int Jmin = T[0] > 0 ? (T[1] > 0 ? min(J0[0], J0[1]) : J0[0]) : J0[1];
-    const int U = (T[0] > 0 || T[1] > 0)
+    const int W = (T[0] > 0 || T[1] > 0)
                       ? max(T[0] > 0 ? J0[0] + T[0] : 0, T[1] > 0 ? J0[1] + T[1] : 0) - Jmin
                       : 0;
+    const int U = SINK ? SU + W : W;       // steps of the pair's stream
+    if constexpr (SINK) {                  // T[g]: all steps of query tile g
+        T[0] += S0;
+        T[1] += S1;
+    }
 
     if (threadIdx.x == 0) {
         if ((smem_addr(smem) & 1023u) != 0) report_error(3);
@@ -245,7 +284,7 @@ __device__ __forceinline__ void fwd_body(const CUtensorMap* tmQ_, const CUtensor
             for (int u = 0; u < U; ++u) {
                 const int s = u % C::STAGES;
                 const int f = u / C::STAGES;
-                const int krow = (Jmin + u) * C::BN;
+                const int krow = (!SINK ? Jmin + u : u < SU ? SB + u : Jmin + u - SU) * C::BN;
                 if (f > 0 && !bounded_wait(&bars->k_empty[s], (f - 1) & 1, abort, lim)) break;
                 mbar_arrive_expect_tx(&bars->k_full[s], C::TILE);
                 for (int ch = 0; ch < C::NCH; ++ch)
@@ -333,17 +372,22 @@ __device__ __forceinline__ void fwd_body(const CUtensorMap* tmQ_, const CUtensor
                         sdesc_at(b, static_cast<uint32_t>((ks * C::KSTEP * C::SWB) >> 4)), idPV,
                         (accumulate || ks > 0) ? 1u : 0u);
             };
-            // Stream step u holds key tile Jmin + u. Query tile g uses steps [J0[g] - Jmin,
+            // Stream step u holds key tile Jmin + u (behind SU steps of sink tiles). Query tile g uses steps [J0[g] - Jmin,
             // J0[g] - Jmin + T[g]); its S for step u+1 is issued during step u (or, for its first
             // tile, before the loop / at the end of step u), so every S reading K tile u+1 is
             // issued before k_empty of that tile is committed.
             const int s0[2] = {J0[0] - Jmin, J0[1] - Jmin};
-            auto active = [&](int g, int u) { return T[g] > 0 && u >= s0[g] && u < s0[g] + T[g]; };
+            auto active = [&](int g, int u) {
+                if constexpr (SINK)
+                    return u < SU ? sinks_of(g) > 0
+                                  : u - SU >= s0[g] && u - SU < s0[g] + (T[g] - sinks_of(g));
+                return T[g] > 0 && u >= s0[g] && u < s0[g] + T[g];
+            };
             if (ok) ok = wait_k(0);
             if (ok) {
                 if (elect_one()) {
                     for (int g = 0; g < 2; ++g)
-                        if (T[g] > 0 && s0[g] == 0) {
+                        if (SINK ? active(g, 0) : T[g] > 0 && s0[g] == 0) {
                             issue_s(g, 0);
                             mma_commit(&bars->s_full[g]);
                         }
@@ -364,7 +408,7 @@ __device__ __forceinline__ void fwd_body(const CUtensorMap* tmQ_, const CUtensor
                 };
                 for (int g = 0; g < 2 && ok; ++g) {
                     if (!active(g, u)) continue;
-                    const int t = u - s0[g];
+                    const int t = SINK ? (u < SU ? u : sinks_of(g) + u - SU - s0[g]) : u - s0[g];
                     // the softmax hands over P in two halves of 64 keys: the first half's P·V
                     // runs while the second half's exponentials are computed
                     if (!bounded_wait_warp(&bars->p_half[g], t & 1, abort, lim)) { ok = false; break; }
@@ -374,10 +418,10 @@ __device__ __forceinline__ void fwd_body(const CUtensorMap* tmQ_, const CUtensor
                     __syncwarp();
                     if (!bounded_wait_warp(&bars->p_full[g], t & 1, abort, lim)) { ok = false; break; }
                     tc_fence_after();
-                    const bool more = t + 1 < T[g];
+                    const bool more = SINK ? active(g, u + 1) : t + 1 < T[g];
                     if (elect_one()) {
                         issue_pv(g, u, 1, true);
-                        if (!more) mma_commit(&bars->o_done[g]);
+                        if (SINK ? t + 1 == T[g] : !more) mma_commit(&bars->o_done[g]);
                     }
                     __syncwarp();
                     if (more) {
@@ -392,7 +436,9 @@ __device__ __forceinline__ void fwd_body(const CUtensorMap* tmQ_, const CUtensor
                 if (!ok) break;
                 if (u + 1 < U) {
                     for (int g = 0; g < 2 && ok; ++g)
-                        if (T[g] > 0 && s0[g] == u + 1) {      // first tile of g is the next one
+                        // first tile of g (or of its window, behind the sinks) is the next one
+                        if (SINK ? active(g, u + 1) && !active(g, u)
+                                 : T[g] > 0 && s0[g] == u + 1) {
                             if (!wait_k(u + 1)) { ok = false; break; }
                             if (elect_one()) {
                                 issue_s(g, u + 1);
@@ -443,7 +489,7 @@ __device__ __forceinline__ void fwd_body(const CUtensorMap* tmQ_, const CUtensor
         float l = 0.f;         // running sum of exp2(.. - m)
         bool ok = true;
         for (int t = 0; t < T[g]; ++t) {
-            const int jj = J0[g] + t;
+            const int jj = SINK && t < sinks_of(g) ? SB + t : J0[g] + t - sinks_of(g);
             ok = bounded_wait(&bars->s_full[g], t & 1, abort, lim);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -456,12 +502,14 @@ __device__ __forceinline__ void fwd_body(const CUtensorMap* tmQ_, const CUtensor
             tmem_ld_wait();
             reg_fence<128>(u);
             const int kbase = jj * C::BN;
-            const bool edge = kbase < full_lo || kbase > full_hi;
+            const bool edge = (kbase < full_lo && (!SINK || kbase > mk.ns - C::BN)) ||
+                              kbase > full_hi;
             if (edge) {
 #pragma unroll
                 for (int c = 0; c < 128; ++c) {
                     const int kidx = kbase + c;
-                    if (kidx < klo || kidx > khi) u[c] = __float_as_uint(-INFINITY);
+                    if ((kidx < klo && (!SINK || kidx >= mk.ns)) || kidx > khi)
+                        u[c] = __float_as_uint(-INFINITY);
                 }
             }
             float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
@@ -741,6 +789,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     fwd_body<D, false, true>(&tmQ, &tmK, &tmV, p);
 }
 
+// Windows with sinks, one CTA per tile pair or clusters that share its key tiles.
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    fwd_bf16_sink_kernel(const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const FwdKParams p) {
+    fwd_body<D, false, SPLIT, false, true>(&tmQ, &tmK, &tmV, p);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     fwd_fp8_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -858,7 +915,7 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t stream) {
     if ((e = make_tmap(&mv, a.v, esize, BHkv, a.nk, D, 128, a.kv_rows)) != cudaSuccess) return e;
     void (*kern)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const FwdKParams);
     if constexpr (F8) kern = fwd_fp8_kernel<D>;
-    else kern = fwd_bf16_kernel<D>;
+    else kern = a.ns > 0 ? fwd_bf16_sink_kernel<D, false> : fwd_bf16_kernel<D>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     FwdKParams kp;
@@ -867,7 +924,7 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t stream) {
     kp.BH = BH;
     const int qtiles = (a.nq + 127) / 128;
     kp.n_pairs = (qtiles + 1) / 2;
-    kp.mask = MaskSpec{a.nq, a.nk, a.wl, a.wr, static_cast<long long>(a.nk) - a.nq};
+    kp.mask = MaskSpec{a.nq, a.nk, a.wl, a.wr, static_cast<long long>(a.nk) - a.nq, a.ns};
     kp.kv_group = a.H / a.Hkv;
     // heads per group: K and V of one head take 4·nk·d bytes; keep a group's within ~32 MB of L2
     {
@@ -899,7 +956,9 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t stream) {
         kern<<<static_cast<unsigned>(grid), kFwdThreads, C::SMEM, stream>>>(mq, mk, mv, kp);
         return cudaGetLastError();
     }
-    constexpr auto skern = split_kernel<D, F8>();
+    auto skern = split_kernel<D, F8>();
+    if constexpr (!F8)
+        if (a.ns > 0) skern = fwd_bf16_sink_kernel<D, true>;
     e = cudaFuncSetAttribute(skern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_SPLIT);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

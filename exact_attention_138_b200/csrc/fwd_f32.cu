@@ -26,6 +26,7 @@
 // the same rule that joins two softmax blocks (weights 2^(m_s - M), M the largest m_s), each CTA
 // finishing a slice of the rows. No global scratch and no second launch are needed.
 #include <cooperative_groups.h>
+#include <limits.h>
 
 #include "kernels.h"
 #include "sm100_ptx.cuh"
@@ -91,11 +92,11 @@ __device__ __forceinline__ void load_rows(float* dst, int ld, const float* src, 
 // Online-softmax step of one thread for one key tile: s (raw scores of rows ty + i·BM/4, keys
 // tx + 8·jj) becomes P = 2^(s·sl2 - m) with m the rows' new running maxima (base 2); l and the
 // output accumulator (column pairs) are rescaled. MASK: keys outside a row's [klo, khi] are
-// dropped.
+// dropped, but for those below ns (INT_MIN: none).
 template <bool MASK, int OC2>
 __device__ __forceinline__ void softmax_tile(float (&s)[4][8], float (&m)[4], float (&l)[4],
                                              uint64_t (&acc)[4][OC2], const int (&klo)[4],
-                                             const int (&khi)[4], int kbase, float sl2,
+                                             const int (&khi)[4], int ns, int kbase, float sl2,
                                              unsigned wmask) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -104,7 +105,7 @@ __device__ __forceinline__ void softmax_tile(float (&s)[4][8], float (&m)[4], fl
         for (int jj = 0; jj < 8; ++jj) {
             if constexpr (MASK) {
                 const int kidx = kbase + 8 * jj;
-                if (kidx < klo[i] || kidx > khi[i]) s[i][jj] = -INFINITY;
+                if ((kidx < klo[i] && kidx >= ns) || kidx > khi[i]) s[i][jj] = -INFINITY;
             }
             mx = fmaxf(mx, s[i][jj]);
         }
@@ -136,7 +137,8 @@ __device__ __forceinline__ void softmax_tile(float (&s)[4][8], float (&m)[4], fl
     }
 }
 
-template <int D>
+// SINK: the first mk.ns keys stay visible; the key tiles that hold them come before the window's.
+template <int D, bool SINK>
 __global__ void __launch_bounds__(128, F32Cfg<D>::MIN_BLOCKS)
     fwd_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K,
                    const float* __restrict__ V, float* __restrict__ O, float* __restrict__ lse,
@@ -182,13 +184,23 @@ __global__ void __launch_bounds__(128, F32Cfg<D>::MIN_BLOCKS)
     // key tiles that hold a key some row of this tile sees; this CTA takes share `rank` of them
     long long tlo, thi;
     visible_keys(mk, q0, qlast, tlo, thi);
-    const int t_begin = tlo <= thi ? static_cast<int>(tlo / kBN) : 0;
-    const int t_count = tlo <= thi ? static_cast<int>(thi / kBN) + 1 - t_begin : 0;
-    const int kt0 = t_begin + static_cast<int>(static_cast<long long>(t_count) * rank / split);
-    const int kt1 = t_begin + static_cast<int>(static_cast<long long>(t_count) * (rank + 1) / split);
+    int t_begin = tlo <= thi ? static_cast<int>(tlo / kBN) : 0;
+    int t_count = tlo <= thi ? static_cast<int>(thi / kBN) + 1 - t_begin : 0;
+    int NS = 0;                  // sink tiles before the window's: list positions [0, NS)
+    if constexpr (SINK) {
+        if (t_count > 0) {
+            NS = sink_tiles(mk, kBN);
+            t_count += min(NS, t_begin);
+            if (t_begin <= NS) t_begin = NS = 0;             // one range from key 0
+        }
+    }
+    // this CTA's share of the list; position x holds tile_at(x)
+    const int kt0 = (SINK ? 0 : t_begin) + static_cast<int>(static_cast<long long>(t_count) * rank / split);
+    const int kt1 = (SINK ? 0 : t_begin) + static_cast<int>(static_cast<long long>(t_count) * (rank + 1) / split);
+    auto tile_at = [&](int x) { return !SINK ? x : (x < NS ? x : t_begin + x - NS); };
 
     auto load_kv = [&](int kt, int buf) {
-        const int k0 = kt * kBN;
+        const int k0 = tile_at(kt) * kBN;
         const size_t g = kvbase + static_cast<size_t>(k0) * D;
         load_rows<D>(fsm + C::K_OFF + buf * kBN * QP, QP, K + g, kBN, nk - k0, tid, nthr);
         load_rows<D>(fsm + C::V_OFF + buf * kBN * D, D, V + g, kBN, nk - k0, tid, nthr);
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__(128, F32Cfg<D>::MIN_BLOCKS)
         __syncthreads();
         const float* Ks = fsm + C::K_OFF + buf * kBN * QP;
         const float* Vs = fsm + C::V_OFF + buf * kBN * D;
-        const int k0 = kt * kBN;
+        const int k0 = tile_at(kt) * kBN;
 
         // S = Q K^T for rows ty + R4·i, keys tx + 8·jj: each 16-byte read of Q and of K is two
         // fp32 pairs, so one packed FMA does two products and each score carries two partial
@@ -262,10 +274,10 @@ __global__ void __launch_bounds__(128, F32Cfg<D>::MIN_BLOCKS)
         }
 
         // online softmax (8 threads share a row); the mask only where some row misses a key
-        if (all_lo <= k0 && k0 + kBN - 1 <= all_hi)
-            softmax_tile<false, OC2>(s, m, l, acc, klo, khi, k0 + tx, sl2, wmask);
+        if ((all_lo <= k0 || (SINK && k0 + kBN <= mk.ns)) && k0 + kBN - 1 <= all_hi)
+            softmax_tile<false, OC2>(s, m, l, acc, klo, khi, INT_MIN, k0 + tx, sl2, wmask);
         else
-            softmax_tile<true, OC2>(s, m, l, acc, klo, khi, k0 + tx, sl2, wmask);
+            softmax_tile<true, OC2>(s, m, l, acc, klo, khi, SINK ? mk.ns : INT_MIN, k0 + tx, sl2, wmask);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -412,7 +424,7 @@ long long f32_max_active_clusters(int bm, int split, int sms, int per_sm, cudaSt
         return fallback;
     }
     if (cap != cudaStreamCaptureStatusNone) return fallback;
-    if (cudaFuncSetAttribute(fwd_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(fwd_f32_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              F32Cfg<D>::SMEM) != cudaSuccess) {
         (void)cudaGetLastError();
         return fallback;
@@ -429,7 +441,7 @@ long long f32_max_active_clusters(int bm, int split, int sms, int per_sm, cudaSt
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fwd_f32_kernel<D>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, fwd_f32_kernel<D, false>, &cfg) != cudaSuccess || n < 1) {
         (void)cudaGetLastError();
         return fallback;
     }
@@ -465,7 +477,8 @@ F32Plan plan_f32(const MaskSpec& mk, long long bh, int per_sm, cudaStream_t stre
             const long long b = a + bm - 1 < mk.nq - 1 ? a + bm - 1 : mk.nq - 1;
             visible_keys(mk, a, b, lo, hi);
             if (lo <= hi) {
-                const int c = static_cast<int>(hi / kBN - lo / kBN + 1);
+                const int lt = static_cast<int>(lo / kBN), s = sink_tiles(mk, kBN);
+                const int c = static_cast<int>(hi / kBN) + 1 - lt + (s < lt ? s : lt);
                 if (c > max_tiles) max_tiles = c;
             }
         }
@@ -498,12 +511,12 @@ F32Plan plan_f32(const MaskSpec& mk, long long bh, int per_sm, cudaStream_t stre
 template <int D>
 cudaError_t launch_fwd_f32_d(const FwdArgs& a, cudaStream_t stream) {
     using C = F32Cfg<D>;
-    cudaError_t e = cudaFuncSetAttribute(fwd_f32_kernel<D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    const auto kern = a.ns > 0 ? fwd_f32_kernel<D, true> : fwd_f32_kernel<D, false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     const long long bh = static_cast<long long>(a.B) * a.H;
     if (bh > 65535) return cudaErrorInvalidConfiguration;
-    const MaskSpec mk{a.nq, a.nk, a.wl, a.wr, static_cast<long long>(a.nk) - a.nq};
+    const MaskSpec mk{a.nq, a.nk, a.wl, a.wr, static_cast<long long>(a.nk) - a.nq, a.ns};
     const F32Plan plan = plan_f32<D>(mk, bh, f32_ctas_per_sm<D>(), stream);
     const int nqt = (a.nq + plan.bm - 1) / plan.bm;
     const int split = plan.split;
@@ -520,7 +533,7 @@ cudaError_t launch_fwd_f32_d(const FwdArgs& a, cudaStream_t stream) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fwd_f32_kernel<D>, static_cast<const float*>(a.q),
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<const float*>(a.q),
                               static_cast<const float*>(a.k), static_cast<const float*>(a.v),
                               static_cast<float*>(a.o), a.lse, mk, nqt, split, a.scale,
                               a.H / a.Hkv);

@@ -15,10 +15,14 @@ namespace attn {
 // contiguous range, and the queries that see a block of keys do too; host and device derive the
 // tile ranges of both passes from the functions below, so the passes agree on which (query tile,
 // key tile) pairs meet.
+// Sinks: with ns > 0 the first ns keys stay visible beyond the left bound (key j is visible iff
+// j <= i + off + wr and (j >= i + off - wl or j < ns)); a query's keys are then the window's range
+// plus, where that begins later, [0, ns). The functions of the window below ignore ns.
 struct MaskSpec {
     int nq, nk;
     int wl, wr;
     long long off;
+    int ns = 0;
 };
 
 __host__ __device__ inline long long floor_div(long long a, long long b) {
@@ -69,6 +73,31 @@ __host__ __device__ inline int last_key_tile(const MaskSpec& m, long long a, int
     return hi < 0 ? 0 : static_cast<int>(hi / bk);
 }
 
+// Key tiles of `bk` keys that hold a sink.
+__host__ __device__ inline int sink_tiles(const MaskSpec& m, int bk) {
+    return static_cast<int>((static_cast<long long>(m.ns < m.nk ? m.ns : m.nk) + bk - 1) / bk);
+}
+
+// Query tiles [i0, i1) of `bq` rows that meet key tile j of `bk` keys: every later query sees a
+// tile that holds a sink.
+__host__ __device__ inline void query_tiles_of_key_tile(const MaskSpec& m, long long j, int bk,
+                                                        int bq, int& i0, int& i1) {
+    MaskSpec w = m;
+    if (j < sink_tiles(m, bk)) w.wl = -1;
+    const long long e = j * bk + bk - 1;
+    visible_query_tiles(w, j * bk, e < m.nk - 1 ? e : m.nk - 1, bq, i0, i1);
+}
+
+// Key tiles above j that meet the query tile of rows [a, a + bq), which meets key tile j itself:
+// the window's tiles, and the sink tiles that lie before them.
+__host__ __device__ inline int key_tiles_above(const MaskSpec& m, long long a, int bq, int bk,
+                                               int j) {
+    const int first = first_key_tile(m, a, bk), last = last_key_tile(m, a, bq, bk);
+    if (j >= first) return last - j;
+    const int s = sink_tiles(m, bk);
+    return last - first + 1 + ((s < first ? s : first) - 1 - j);
+}
+
 __host__ __device__ inline int clamp_int(long long x) {
     return x < -0x7fffffffLL ? -0x7fffffff : (x > 0x7fffffffLL ? 0x7fffffff : static_cast<int>(x));
 }
@@ -85,6 +114,7 @@ struct FwdArgs {
     int wl, wr;       // visible window (see MaskSpec)
     float q_descale, k_descale, v_descale;   // E4M3 inputs only: real value = stored · descale
     uint64_t timeout_ns;
+    int ns = 0;       // sinks (see MaskSpec); 0 when wl is unbounded
     // >= 0: o and lse are a running fp32 result (o_acc, lse_acc) that the launch folds its own
     // into (bf16 inputs); 1: the first such launch (initialise, do not read)
     int acc_first = -1;
@@ -127,7 +157,16 @@ struct BwdArgs {
     // launch's queries are its rows [q_row0, q_row0 + nq) (q_row0 a multiple of 64).
     long long q_rows = 0, kv_rows = 0;
     int ws_rows = 0, q_row0 = 0;
+    // Sinks (see MaskSpec): the queries of each key tile that holds one are shared by sink_parts
+    // CTAs, whose dK, dV partials (B·Hkv, sink tiles, parts, 128 rows, d fp32; all dK, then all dV)
+    // lie in sink_buf and are summed in a launch of their own.
+    int ns = 0, sink_parts = 0;
+    float* sink_buf = nullptr;
 };
+
+// CTAs that share the queries of one sink key tile in the backward pass: about as many query
+// tiles each as a key tile of the window meets.
+int bwd_sink_parts(int H, int Hkv, int nq, int nk, int d, int wl, int wr);
 
 // Encodes a 3-D tensor map over a (B*H, n, d) tensor of `esize`-byte elements (2: bf16, 1: 8-bit)
 // with a box of (chunk, box_rows, 1), chunk = min(d, 128 / esize) elements, and the swizzle that

@@ -149,6 +149,18 @@ int attn_fwd_ex(const void* q, const void* k, const void* v, void* o, float* lse
                 int B, int H, int Hkv, int nq, int nk, int d, float scale,
                 int window_left, int window_right, int dtype, void* stream);
 
+/* Sliding window with sinks: attn_fwd_ex, with the first n_sink keys visible beyond the window's
+ * left bound (the sink + window pattern of "Attention Mechanism: Revolusi Representasi Sequence",
+ * §4.5 "Sparse Attention" and its list of attention sinks: a window alone loses the first tokens,
+ * which take much of every row's weight). Key j is visible to query i iff, with off = nk - nq,
+ *     j <= i + off + window_right   and   (j >= i + off - window_left  or  j < n_sink);
+ * a negative bound is none, so n_sink changes nothing when window_left is negative, and n_sink = 0
+ * is attn_fwd_ex. n_sink may exceed nk. bf16 and fp32; one launch, no library memory.
+ * Errors as attn_fwd_ex; n_sink < 0 is ATTN_ERR_INVALID. */
+int attn_fwd_sink(const void* q, const void* k, const void* v, void* o, float* lse,
+                  int B, int H, int Hkv, int nq, int nk, int d, float scale,
+                  int window_left, int window_right, int n_sink, int dtype, void* stream);
+
 /* Backward pass (bf16 only). Inputs q, k, v, o, dO (bf16) and lse (fp32, from attn_fwd with the
  * same scale and causal flag). Writes dq, dk, dv (bf16). The workspace (caller-owned device
  * memory of at least attn_bwd_workspace_bytes() bytes, 256-byte aligned) is overwritten.
@@ -180,6 +192,18 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
                 int B, int H, int Hkv, int nq, int nk, int d, float scale,
                 int window_left, int window_right, int dtype, int deterministic,
                 void* workspace, size_t ws_bytes, void* stream);
+
+/* Backward pass of attn_fwd_sink (bf16 only): attn_bwd_ex on that mask. A sink's dk, dv sum over every
+ * later query; the query tiles of the key tiles that hold a sink are shared by several CTAs whose
+ * fp32 partials the workspace holds and which are added in a fixed order (the deterministic mode
+ * repeats bit for bit). The workspace is attn_bwd_sink_workspace_bytes() with the same arguments. */
+size_t attn_bwd_sink_workspace_bytes(int B, int H, int Hkv, int nq, int nk, int d, int window_left,
+                                     int window_right, int n_sink, int deterministic);
+int attn_bwd_sink(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                  const float* lse, void* dq, void* dk, void* dv,
+                  int B, int H, int Hkv, int nq, int nk, int d, float scale,
+                  int window_left, int window_right, int n_sink, int dtype, int deterministic,
+                  void* workspace, size_t ws_bytes, void* stream);
 
 /* Backward pass without a caller workspace, for callers that cannot allocate device memory where
  * they run it (e.g. code inside a host framework that owns all device allocations, or a loop that
