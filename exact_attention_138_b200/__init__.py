@@ -618,3 +618,19 @@ def forward_fp8(q, k, v, q_descale=1.0, k_descale=1.0, v_descale=1.0, causal=Fal
                       _stream_handle(stream))
     _check(rc, "attn_fwd_fp8")
     return out, lse
+
+
+# ---------------------------------------------------------------- the 4-bit paged cache (kvcache.py)
+_KVCACHE = ("attn_kv4_append", "attn_kv4_attend", "attn_kv4_gather", "attn_kv4_page_bytes",
+            "attn_kv4_workspace_bytes", "kv4_append", "kv4_attend", "kv4_gather", "kv4_pool")
+
+
+def __getattr__(name):
+    """The names of kvcache.py, which needs torch, on their first use (the rest of this module imports
+    without torch)."""
+    if name in _KVCACHE:
+        from . import kvcache
+        for n in _KVCACHE:
+            globals()[n] = getattr(kvcache, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

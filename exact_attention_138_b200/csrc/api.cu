@@ -8,6 +8,7 @@
 
 #include "../../include/attn.h"
 #include "kernels.h"
+#include "kv4.h"
 #include "ring.h"
 #include "sm100_ptx.cuh"
 
@@ -502,6 +503,97 @@ int attn_ring_accumulate(float* acc, const void* part, long long count, int part
     return to_code(launch_ring_accumulate(acc, part, count, part_dtype == ATTN_BF16,
                                           first ? 1 : 0, out, out_dtype == ATTN_BF16,
                                           static_cast<cudaStream_t>(stream)));
+}
+
+// Arguments of every call on a 4-bit cache.
+static int check_pool(Kv4Pool& p, const void* pool, const int* table, const int* seqs, int pages,
+                      int slots, int max_pages, int page_size, int B, int Hkv, int d) {
+    if (!pool || !table) return ATTN_ERR_INVALID;
+    if (!aligned16(pool)) return ATTN_ERR_INVALID;
+    if (d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+    if (page_size < kKv4Block || page_size % kKv4Block != 0 || page_size > 65536)
+        return ATTN_ERR_INVALID;
+    if (pages < 1 || slots < 1 || max_pages < 1 || B < 1 || B > 65535 || Hkv < 1 || Hkv > 65535)
+        return ATTN_ERR_INVALID;
+    if (static_cast<long long>(max_pages) * page_size > kMaxSeq) return ATTN_ERR_INVALID;
+    if (!seqs && B > slots) return ATTN_ERR_INVALID;
+    p = Kv4Pool{static_cast<uint8_t*>(const_cast<void*>(pool)), table, seqs, pages, slots, max_pages,
+                page_size, Hkv, d};
+    return ATTN_OK;
+}
+
+size_t attn_kv4_page_bytes(int page_size, int Hkv, int d) {
+    if (page_size < kKv4Block || page_size % kKv4Block != 0 || Hkv < 1 ||
+        (d != 32 && d != 64 && d != 128))
+        return 0;
+    return static_cast<size_t>(page_size / kKv4Block) * Hkv * kv4_block_bytes(d);
+}
+
+static int kv4_rows(Kv4RowsArgs& a, const void* pool, const int* table, const int* seqs,
+                    const int* start, const int* counts, const void* k, const void* v, int pages,
+                    int slots, int max_pages, int page_size, int B, int Hkv, int n, int d) {
+    if (!start || !k || !v) return ATTN_ERR_INVALID;
+    int rc = check_pool(a.pool, pool, table, seqs, pages, slots, max_pages, page_size, B, Hkv, d);
+    if (rc) return rc;
+    if (n < 1 || n > kMaxSeq || !aligned16(k) || !aligned16(v)) return ATTN_ERR_INVALID;
+    a.start = start;
+    a.counts = counts;
+    a.k = const_cast<void*>(k);
+    a.v = const_cast<void*>(v);
+    a.B = B;
+    a.n = n;
+    return ATTN_OK;
+}
+
+int attn_kv4_append(void* pool, const int* table, const int* seqs, const int* start,
+                    const int* counts, const void* k, const void* v, int pages, int slots,
+                    int max_pages, int page_size, int B, int Hkv, int n, int d, void* stream) {
+    Kv4RowsArgs a;
+    int rc = kv4_rows(a, pool, table, seqs, start, counts, k, v, pages, slots, max_pages, page_size,
+                      B, Hkv, n, d);
+    return rc ? rc : to_code(launch_kv4_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_kv4_gather(const void* pool, const int* table, const int* seqs, const int* start,
+                    const int* counts, void* k, void* v, int pages, int slots, int max_pages,
+                    int page_size, int B, int Hkv, int n, int d, void* stream) {
+    Kv4RowsArgs a;
+    int rc = kv4_rows(a, pool, table, seqs, start, counts, k, v, pages, slots, max_pages, page_size,
+                      B, Hkv, n, d);
+    return rc ? rc : to_code(launch_kv4_gather(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_kv4_workspace_bytes(int H, int Hkv, int nq, int d) {
+    if (H < 1 || Hkv < 1 || H % Hkv != 0 || nq < 1 || d < 1) return 0;
+    return kv4_attend_ws_bytes(H, Hkv, nq, d);
+}
+
+int attn_kv4_attend(const void* q, const void* pool, const int* table, const int* seqs,
+                    const int* lens, void* o, float* lse, int pages, int slots, int max_pages,
+                    int page_size, int B, int H, int Hkv, int nq, int d, float scale,
+                    int window_left, int window_right, int n_sink, void* workspace, size_t ws_bytes,
+                    void* stream) {
+    if (!q || !lens || !o || !lse) return ATTN_ERR_INVALID;
+    int rc = validate_common(B, H, nq, d, scale, ATTN_BF16);
+    if (rc) return rc;
+    Kv4AttendArgs a;
+    if ((rc = check_pool(a.pool, pool, table, seqs, pages, slots, max_pages, page_size, B, Hkv, d)))
+        return rc;
+    if (H % Hkv != 0 || n_sink < 0) return ATTN_ERR_INVALID;
+    if (static_cast<long long>(B) * H * nq > 0x7fffffffLL) return ATTN_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_INVALID;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_INVALID;
+    if (ws_bytes < kv4_attend_ws_bytes(H, Hkv, nq, d)) return ATTN_ERR_WORKSPACE;
+    a.lens = lens;
+    a.q = q; a.o = o; a.lse = lse;
+    a.B = B; a.H = H; a.nq = nq;
+    a.scale = scale;
+    a.wl = window_left < 0 ? -1 : window_left;
+    a.wr = window_right < 0 ? -1 : window_right;
+    a.ns = a.wl < 0 ? 0 : n_sink;
+    a.ws = static_cast<float*>(workspace);
+    a.timeout_ns = static_cast<uint64_t>(g_timeout_us.load()) * 1000ull;
+    return to_code(launch_kv4_attend(a, static_cast<cudaStream_t>(stream)));
 }
 
 void attn_set_bwd_phase_events(void* const* events) {

@@ -6,3 +6,4 @@
 #include "bwd_bf16.cu"
 #include "bwd_noalloc.cu"
 #include "ring.cu"
+#include "kv4.cu"

@@ -1,0 +1,208 @@
+"""A paged K/V cache in 4 bits: quantising rows into it, reading them back and attending to it
+(attn_kv4_* of include/attn.h, csrc/kv4.cu). Like the rest of the package this module only marshals
+arguments; device memory and streams come from PyTorch.
+
+    pool = kv4_pool(pages, kv_heads, page_size, d)            # uint8 (pages, kv_heads, bytes)
+    table: int32 (slots, max_pages), the page of every page_size tokens of a sequence, -1: none
+    kv4_append(pool, table, start, k, v)                      # rows of k, v -> tokens start + row
+    o, lse = kv4_attend(q, pool, table, lens, window=(1024, 0), sinks=4)
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import AttnError, _lib, _sinks
+
+_vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_lib.attn_kv4_page_bytes.restype = _sz
+_lib.attn_kv4_page_bytes.argtypes = [_i, _i, _i]
+_lib.attn_kv4_append.restype = _i
+_lib.attn_kv4_append.argtypes = [_vp] * 7 + [_i] * 8 + [_vp]
+_lib.attn_kv4_gather.restype = _i
+_lib.attn_kv4_gather.argtypes = [_vp] * 7 + [_i] * 8 + [_vp]
+_lib.attn_kv4_workspace_bytes.restype = _sz
+_lib.attn_kv4_workspace_bytes.argtypes = [_i] * 4
+_lib.attn_kv4_attend.restype = _i
+_lib.attn_kv4_attend.argtypes = [_vp] * 7 + [_i] * 9 + [_f, _i, _i, _i, _vp, _sz, _vp]
+
+
+# ---------------------------------------------------------------- raw C entry points
+def attn_kv4_page_bytes(page_size, Hkv, d) -> int:
+    return _lib.attn_kv4_page_bytes(page_size, Hkv, d)
+
+
+def attn_kv4_append(pool, table, seqs, start, counts, k, v, pages, slots, max_pages, page_size, B,
+                    Hkv, n, d, stream) -> int:
+    return _lib.attn_kv4_append(pool, table, seqs, start, counts, k, v, pages, slots, max_pages,
+                                page_size, B, Hkv, n, d, stream)
+
+
+def attn_kv4_gather(pool, table, seqs, start, counts, k, v, pages, slots, max_pages, page_size, B,
+                    Hkv, n, d, stream) -> int:
+    return _lib.attn_kv4_gather(pool, table, seqs, start, counts, k, v, pages, slots, max_pages,
+                                page_size, B, Hkv, n, d, stream)
+
+
+def attn_kv4_workspace_bytes(H, Hkv, nq, d) -> int:
+    return _lib.attn_kv4_workspace_bytes(H, Hkv, nq, d)
+
+
+def attn_kv4_attend(q, pool, table, seqs, lens, o, lse, pages, slots, max_pages, page_size, B, H, Hkv,
+                    nq, d, scale, window_left, window_right, n_sink, workspace, ws_bytes, stream) -> int:
+    return _lib.attn_kv4_attend(q, pool, table, seqs, lens, o, lse, pages, slots, max_pages,
+                                page_size, B, H, Hkv, nq, d, scale, window_left, window_right, n_sink,
+                                workspace, ws_bytes, stream)
+
+
+# ---------------------------------------------------------------- torch-tensor wrappers
+def _tensors(where, *ts):
+    """Packed CUDA tensors on the current device: kernels are launched there, and a host or a strided
+    tensor's pointer must never reach one."""
+    dev = torch.cuda.current_device() if ts[0].is_cuda else None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda or t.get_device() != dev:
+            raise ValueError(f"{where}: tensors must be on the current CUDA device")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: tensors must be contiguous")
+    return dev
+
+
+def _is(where, name, t, dtype, *shape):
+    """t must have this dtype and shape (None: any size of that dimension)."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(
+            s is not None and s != x for s, x in zip(shape, t.shape)):
+        raise ValueError(f"{where}: {name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _raw_stream(stream, dev, *made):
+    """The stream's handle; tensors made here on the current stream are kept until `stream` is done."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    for t in made:
+        t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _page_size(where, pool, d):
+    """Tokens of a page of the pool (pages, kv_heads, bytes)."""
+    if pool.dtype != torch.uint8 or pool.dim() != 3:
+        raise ValueError(f"{where}: the pool must be uint8 (pages, kv_heads, bytes)")
+    if d not in (32, 64, 128):
+        raise AttnError(2, where)
+    if pool.shape[2] < 1 or pool.shape[2] % (20 * d):
+        raise ValueError(f"{where}: a page and head of {pool.shape[2]} bytes holds no blocks of {20 * d}")
+    return pool.shape[2] // (20 * d) * 16
+
+
+def _rows(where, pool, table, d, B, start, counts, seqs):
+    page = _page_size(where, pool, d)
+    _is(where, "table", table, torch.int32, None, None)
+    _is(where, "start", start, torch.int32, B)
+    for name, t in (("counts", counts), ("seqs", seqs)):
+        if t is not None:
+            _is(where, name, t, torch.int32, B)
+    return page
+
+
+def kv4_pool(pages, kv_heads, page_size, d, device=None):
+    """An uninitialised pool: uint8 (pages, kv_heads, page_size / 16 * 20 d)."""
+    each = attn_kv4_page_bytes(page_size, 1, d)
+    if not each or pages < 1 or kv_heads < 1:
+        raise ValueError("page_size must be a multiple of 16, d 32, 64 or 128, counts 1 or more")
+    return torch.empty((pages, kv_heads, each), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def kv4_append(pool, table, start, k, v, counts=None, seqs=None, stream=None):
+    """Quantises rows [0, counts[i]) (all, without counts) of k, v (B, kv_heads, n, d) bf16 into tokens
+    start[i] + row of table row seqs[i] (i, without seqs). A negative start leaves its entry out, tokens
+    on no page are dropped, and no other token's bits change."""
+    where = "kv4_append"
+    if k.dim() != 4:
+        raise ValueError(f"{where}: k and v must be (B, kv_heads, n, d)")
+    B, Hkv, n, d = k.shape
+    page = _rows(where, pool, table, d, B, start, counts, seqs)
+    _is(where, "k", k, torch.bfloat16, B, pool.shape[1], n, d)
+    _is(where, "v", v, torch.bfloat16, B, Hkv, n, d)
+    dev = _tensors(where, pool, table, start, k, v, counts, seqs)
+    rc = _lib.attn_kv4_append(pool.data_ptr(), table.data_ptr(), _at(seqs), start.data_ptr(),
+                              _at(counts), k.data_ptr(), v.data_ptr(), pool.shape[0], table.shape[0],
+                              table.shape[1], page, B, Hkv, n, d, _raw_stream(stream, dev))
+    if rc:
+        raise AttnError(rc, "attn_kv4_append")
+
+
+def kv4_gather(pool, table, start, n, d, counts=None, seqs=None, k=None, v=None, stream=None):
+    """The values that tokens start[i] .. start[i] + n - 1 of table row seqs[i] stand for, rounded to
+    bf16: k, v (B, kv_heads, n, d). Rows at or beyond counts[i], of entries with a negative start and
+    on no page are zeros."""
+    where = "kv4_gather"
+    B = start.shape[0]
+    page = _rows(where, pool, table, d, B, start, counts, seqs)
+    if n < 1:
+        raise ValueError(f"{where}: n must be 1 or more")
+    dev = _tensors(where, pool, table, start, counts, seqs, k, v)
+    shape = (B, pool.shape[1], n, d)
+    made = [torch.empty(shape, dtype=torch.bfloat16, device=pool.device) if t is None else t for t in (k, v)]
+    for name, t in zip("kv", made):
+        _is(where, name, t, torch.bfloat16, *shape)
+    rc = _lib.attn_kv4_gather(pool.data_ptr(), table.data_ptr(), _at(seqs), start.data_ptr(),
+                              _at(counts), made[0].data_ptr(), made[1].data_ptr(), pool.shape[0],
+                              table.shape[0], table.shape[1], page, B, shape[1], n, d,
+                              _raw_stream(stream, dev, *made))
+    if rc:
+        raise AttnError(rc, "attn_kv4_gather")
+    return made[0], made[1]
+
+
+def kv4_attend(q, pool, table, lens, window=None, sinks=0, scale=None, seqs=None, out=None, lse=None,
+               workspace=None, stream=None):
+    """O, LSE of q (B, H, nq, d) bf16 over the lens[row] tokens of table row seqs[i] (i, without
+    seqs), for the newest tokens of a sequence: query t sits at key position lens - nq + t. window =
+    (left, right) as in `forward`; None is causal, (-1, 0). The first `sinks` tokens stay visible
+    beyond the left bound. Tokens on no page are not seen; a row that sees none gets O = 0, LSE =
+    -inf."""
+    where = "kv4_attend"
+    if q.dim() != 4:
+        raise ValueError(f"{where}: q must be (B, H, nq, d)")
+    B, H, nq, d = q.shape
+    page = _page_size(where, pool, d)
+    pages, Hkv, _ = pool.shape
+    if H % Hkv:
+        raise ValueError(f"{where}: H must be a multiple of the pool's K/V heads")
+    _is(where, "q", q, torch.bfloat16, B, H, nq, d)
+    _is(where, "table", table, torch.int32, None, None)
+    slots, width = table.shape
+    _is(where, "lens", lens, torch.int32, slots)
+    if seqs is not None:
+        _is(where, "seqs", seqs, torch.int32, B)
+    wl, wr = (-1, 0) if window is None else (int(window[0]), int(window[1]))
+    sinks = _sinks(sinks)
+    dev = _tensors(where, q, pool, table, lens, seqs, out, lse, workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, H, nq), dtype=torch.float32, device=q.device)
+    need = _lib.attn_kv4_workspace_bytes(H, Hkv, nq, d)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _is(where, "out", out, torch.bfloat16, B, H, nq, d)
+    _is(where, "lse", lse, torch.float32, B, H, nq)
+    rc = _lib.attn_kv4_attend(q.data_ptr(), pool.data_ptr(), table.data_ptr(), _at(seqs),
+                              lens.data_ptr(), out.data_ptr(), lse.data_ptr(), pages, slots, width,
+                              page, B, H, Hkv, nq, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
+                              wl, wr, sinks, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(),
+                              _raw_stream(stream, dev, out, lse, workspace))
+    if rc:
+        raise AttnError(rc, "attn_kv4_attend")
+    return out, lse

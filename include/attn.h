@@ -308,6 +308,51 @@ int attn_ring_merge(float* o_acc, float* lse_acc, const void* o_part, const floa
 int attn_ring_accumulate(float* acc, const void* part, long long count, int part_dtype, int first,
                          void* out, int out_dtype, void* stream);
 
+/* 4-bit paged K/V cache ("Attention Mechanism: Revolusi Representasi Sequence", §"KV Cache" and its
+ * quantised cache). K and V of past tokens are held as groups of 32 channels of one token and
+ * K/V head: lo = the group's least value, s = bf16((greatest - lo) / 15) (0 below 2^-100),
+ * q = the whole number nearest (x - lo)/s, ties to even, in 0..15; the group stands for lo + s·q. A
+ * group that holds a NaN or an infinity (or whose range exceeds fp32) stands for NaN.
+ *   pool: caller-owned device memory, 16-byte aligned, `pages` pages of attn_kv4_page_bytes() bytes,
+ *     (pages, Hkv, page_size/16, 20·d) bytes: 16 tokens of one head are one block of 20·d bytes (1.25
+ *     bytes per channel of K and V together; the order inside is that of kv4.h). page_size: a
+ *     multiple of 16. d in {32, 64, 128}.
+ *   table: (slots, max_pages) int32, the page that holds tokens [m·page_size, (m+1)·page_size) of each
+ *     sequence, -1: none. seqs: B int32 rows of the table, NULL: entry i is row i. A row outside the
+ *     table has no tokens; a number outside [0, pages) is no page. All int32 arrays lie in device memory.
+ * Every call is asynchronous on `stream`, allocates nothing and can be captured into a graph.
+ *
+ * attn_kv4_append: quantises rows [0, counts[i]) (NULL: n) of k, v (B, Hkv, n, d) bf16 into tokens
+ *   start[i] + row. start[i] < 0 leaves the entry out; tokens on no page are dropped. No other token's
+ *   bits change, nor do pages' bytes that hold no token yet. Entries of one call must not share tokens.
+ * attn_kv4_gather: the same rows back as bf16(lo + s·q); rows at or beyond counts[i], of entries left
+ *   out and on no page are zeros.
+ * attn_kv4_attend: attn_fwd_sink of q (B, H, nq, d) bf16 over each sequence's lens[row] tokens as the
+ *   cache holds them, for the few newest tokens: query t sits at key position lens - nq + t, and
+ *     j <= lens - nq + t + window_right and (j >= lens - nq + t - window_left or j < n_sink).
+ *   Tokens on no page are not seen (so pages that a window has left behind can be freed). o (B, H, nq,
+ *   d) bf16, lse (B, H, nq) fp32; a row that sees no key gets o = 0, lse = -inf. Any nq >= 1 is computed,
+ *   8 (or 16) query rows of a K/V head share one pass over its keys. lens is read on the device:
+ *   one captured call serves growing sequences. The workspace (attn_kv4_workspace_bytes(), 256-byte
+ *   aligned) is overwritten; calls that share one must be ordered.
+ * Errors: null, misaligned (16-byte; start, counts, table, seqs, lens: 4-byte) pointers, sizes below 1,
+ *   B or Hkv > 65535, max_pages·page_size > 2^31 - 257, a page_size that is no multiple of 16, H
+ *   no multiple of Hkv, n_sink < 0, no seqs and B > slots -> ATTN_ERR_INVALID; d -> ATTN_ERR_UNSUPPORTED;
+ *   workspace too small -> ATTN_ERR_WORKSPACE. */
+size_t attn_kv4_page_bytes(int page_size, int Hkv, int d);
+int attn_kv4_append(void* pool, const int* table, const int* seqs, const int* start,
+                    const int* counts, const void* k, const void* v, int pages, int slots,
+                    int max_pages, int page_size, int B, int Hkv, int n, int d, void* stream);
+int attn_kv4_gather(const void* pool, const int* table, const int* seqs, const int* start,
+                    const int* counts, void* k, void* v, int pages, int slots, int max_pages,
+                    int page_size, int B, int Hkv, int n, int d, void* stream);
+size_t attn_kv4_workspace_bytes(int H, int Hkv, int nq, int d);
+int attn_kv4_attend(const void* q, const void* pool, const int* table, const int* seqs,
+                    const int* lens, void* o, float* lse, int pages, int slots, int max_pages,
+                    int page_size, int B, int H, int Hkv, int nq, int d, float scale,
+                    int window_left, int window_right, int n_sink, void* workspace, size_t ws_bytes,
+                    void* stream);
+
 /* Measurement hook. `events` is NULL (recording off, the default) or an array of 4 cudaEvent_t
  * created by the caller. While set, every attn_bwd call records, on its stream, events[0] before
  * its preprocess kernel (D = rowsum(dO∘O)), events[1] before its main kernel, events[2] after
