@@ -28,6 +28,7 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "attn.h")
 ATTN_BF16, ATTN_FP32 = 0, 1
 ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED = 0, 1, 2
 ATTN_ERR_CUDA, ATTN_ERR_TIMEOUT, ATTN_ERR_WORKSPACE = 3, 4, 5
+ATTN_ERR_PAGES = 6
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -620,9 +621,12 @@ def forward_fp8(q, k, v, q_descale=1.0, k_descale=1.0, v_descale=1.0, causal=Fal
     return out, lse
 
 
-# ---------------------------------------------------------------- the 4-bit paged cache (kvcache.py)
+# ---------------------------------------------------------------- the paged cache (kvcache.py)
 _KVCACHE = ("attn_kv4_append", "attn_kv4_attend", "attn_kv4_gather", "attn_kv4_page_bytes",
-            "attn_kv4_workspace_bytes", "kv4_append", "kv4_attend", "kv4_gather", "kv4_pool")
+            "attn_kv4_workspace_bytes", "attn_pages_compact", "attn_pages_copy", "attn_pages_fork",
+            "attn_pages_free", "attn_pages_reserve", "attn_pages_workspace_bytes", "kv4_append",
+            "kv4_attend", "kv4_gather", "kv4_pool", "pages_compact", "pages_copy", "pages_fork",
+            "pages_free", "pages_reserve")
 
 
 def __getattr__(name):

@@ -9,6 +9,7 @@
 #include "../../include/attn.h"
 #include "kernels.h"
 #include "kv4.h"
+#include "pages.h"
 #include "ring.h"
 #include "sm100_ptx.cuh"
 
@@ -165,6 +166,7 @@ const char* attn_error_string(int code) {
         case ATTN_ERR_CUDA: return "CUDA error";
         case ATTN_ERR_TIMEOUT: return "device-side wait timed out";
         case ATTN_ERR_WORKSPACE: return "workspace too small";
+        case ATTN_ERR_PAGES: return "page call refused";
         default: return "unknown error";
     }
 }
@@ -594,6 +596,82 @@ int attn_kv4_attend(const void* q, const void* pool, const int* table, const int
     a.ws = static_cast<float*>(workspace);
     a.timeout_ns = static_cast<uint64_t>(g_timeout_us.load()) * 1000ull;
     return to_code(launch_kv4_attend(a, static_cast<cudaStream_t>(stream)));
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Arguments of every call on a page table; counts of sequences are checked by the callers.
+static int check_pages(PageState& s, int* table, int* lens, int* refs, int pages, int slots,
+                       int max_pages, int page_size) {
+    if (!table || !lens || !refs || !aligned4(table) || !aligned4(lens) || !aligned16(refs))
+        return ATTN_ERR_INVALID;
+    if (pages < 1 || pages > kMaxSeq || slots < 1 || slots > kPagesMaxSlots || max_pages < 1 ||
+        page_size < 1 || static_cast<long long>(max_pages) * page_size > kMaxSeq)
+        return ATTN_ERR_INVALID;
+    s = PageState{table, lens, refs, pages, slots, max_pages, page_size};
+    return ATTN_OK;
+}
+
+int attn_pages_reserve(int* table, int* lens, int* refs, const int* seqs, const int* counts,
+                       int* start, int pages, int slots, int max_pages, int page_size, int n,
+                       void* stream) {
+    PageState s;
+    int rc = check_pages(s, table, lens, refs, pages, slots, max_pages, page_size);
+    if (rc) return rc;
+    if (!seqs || !counts || !start || !aligned4(seqs) || !aligned4(counts) || !aligned4(start) ||
+        n < 1 || n > kPagesMaxSeqs)
+        return ATTN_ERR_INVALID;
+    return to_code(launch_pages_reserve(s, seqs, counts, start, n, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_pages_fork(int* table, int* lens, int* refs, const int* src, const int* dst, int* from,
+                    int* to, int pages, int slots, int max_pages, int page_size, int n,
+                    void* stream) {
+    PageState s;
+    int rc = check_pages(s, table, lens, refs, pages, slots, max_pages, page_size);
+    if (rc) return rc;
+    if (!src || !dst || !from || !to || !aligned4(src) || !aligned4(dst) || !aligned4(from) ||
+        !aligned4(to) || n < 1 || n > kPagesMaxSeqs)
+        return ATTN_ERR_INVALID;
+    return to_code(launch_pages_fork(s, src, dst, from, to, n, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_pages_free(int* table, int* lens, int* refs, const int* seqs, int pages, int slots,
+                    int max_pages, int page_size, int n, int window_left, int n_sink, void* stream) {
+    PageState s;
+    int rc = check_pages(s, table, lens, refs, pages, slots, max_pages, page_size);
+    if (rc) return rc;
+    if (!seqs || !aligned4(seqs) || n < 1 || n_sink < 0) return ATTN_ERR_INVALID;
+    return to_code(launch_pages_free(s, seqs, n, window_left < 0, window_left, n_sink,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_pages_workspace_bytes(int pages) {
+    return pages < 1 ? 0 : (static_cast<size_t>(pages) + 4) * sizeof(int);
+}
+
+int attn_pages_compact(int* table, int* refs, int* from, int* to, int* count, int pages, int slots,
+                       int max_pages, void* workspace, size_t ws_bytes, void* stream) {
+    PageState s;
+    int rc = check_pages(s, table, table, refs, pages, slots, max_pages, 1);
+    if (rc) return rc;
+    if (!from || !to || !count || !aligned4(from) || !aligned4(to) || !aligned4(count) || !workspace ||
+        !aligned16(workspace))
+        return ATTN_ERR_INVALID;
+    if (ws_bytes < attn_pages_workspace_bytes(pages)) return ATTN_ERR_WORKSPACE;
+    return to_code(launch_pages_compact(s, from, to, count, static_cast<int*>(workspace),
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+int attn_pages_copy(void* pool, const int* from, const int* to, const int* count, int layers,
+                    int pages, long long page_bytes, int n, void* stream) {
+    if (!pool || !from || !to || !aligned16(pool) || !aligned4(from) || !aligned4(to) ||
+        !aligned4(count))
+        return ATTN_ERR_INVALID;
+    if (layers < 1 || pages < 1 || n < 1 || page_bytes < 16 || page_bytes % 16 != 0)
+        return ATTN_ERR_INVALID;
+    return to_code(launch_pages_copy(pool, from, to, count, layers, pages, page_bytes, n,
+                                     static_cast<cudaStream_t>(stream)));
 }
 
 void attn_set_bwd_phase_events(void* const* events) {

@@ -7,3 +7,4 @@
 #include "bwd_noalloc.cu"
 #include "ring.cu"
 #include "kv4.cu"
+#include "pages.cu"

@@ -1,11 +1,21 @@
-"""A paged K/V cache in 4 bits: quantising rows into it, reading them back and attending to it
-(attn_kv4_* of include/attn.h, csrc/kv4.cu). Like the rest of the package this module only marshals
+"""A paged K/V cache in 4 bits: quantising rows into it, reading them back, attending to it
+(attn_kv4_* of include/attn.h, csrc/kv4.cu) and its pages (attn_pages_*, csrc/pages.cu). Like the rest of the package this module only marshals
 arguments; device memory and streams come from PyTorch.
 
     pool = kv4_pool(pages, kv_heads, page_size, d)            # uint8 (pages, kv_heads, bytes)
     table: int32 (slots, max_pages), the page of every page_size tokens of a sequence, -1: none
     kv4_append(pool, table, start, k, v)                      # rows of k, v -> tokens start + row
     o, lse = kv4_attend(q, pool, table, lens, window=(1024, 0), sinks=4)
+
+Pages: with lens (slots,) and refs (pages,), int32 like the table and all of it on the device,
+
+    start = pages_reserve(table, lens, refs, page_size, seqs, counts)     # room for new tokens
+    pages_copy(pool, *pages_fork(table, lens, refs, page_size, src, dst)) # sequences that share pages
+    pages_free(table, lens, refs, page_size, seqs)                        # they end
+    pages_free(table, lens, refs, page_size, seqs, window=(1024, 0), sinks=4)  # what no query sees
+    pages_copy(pool, *pages_compact(table, refs))                         # pages in use come first
+
+A call that cannot be served changes nothing; `device_status()` then says ATTN_ERR_PAGES.
 """
 from __future__ import annotations
 
@@ -27,6 +37,18 @@ _lib.attn_kv4_workspace_bytes.restype = _sz
 _lib.attn_kv4_workspace_bytes.argtypes = [_i] * 4
 _lib.attn_kv4_attend.restype = _i
 _lib.attn_kv4_attend.argtypes = [_vp] * 7 + [_i] * 9 + [_f, _i, _i, _i, _vp, _sz, _vp]
+_lib.attn_pages_reserve.restype = _i
+_lib.attn_pages_reserve.argtypes = [_vp] * 6 + [_i] * 5 + [_vp]
+_lib.attn_pages_fork.restype = _i
+_lib.attn_pages_fork.argtypes = [_vp] * 7 + [_i] * 5 + [_vp]
+_lib.attn_pages_free.restype = _i
+_lib.attn_pages_free.argtypes = [_vp] * 4 + [_i] * 7 + [_vp]
+_lib.attn_pages_workspace_bytes.restype = _sz
+_lib.attn_pages_workspace_bytes.argtypes = [_i]
+_lib.attn_pages_compact.restype = _i
+_lib.attn_pages_compact.argtypes = [_vp] * 5 + [_i] * 3 + [_vp, _sz, _vp]
+_lib.attn_pages_copy.restype = _i
+_lib.attn_pages_copy.argtypes = [_vp] * 4 + [_i, _i, ctypes.c_longlong, _i, _vp]
 
 
 # ---------------------------------------------------------------- raw C entry points
@@ -55,6 +77,38 @@ def attn_kv4_attend(q, pool, table, seqs, lens, o, lse, pages, slots, max_pages,
     return _lib.attn_kv4_attend(q, pool, table, seqs, lens, o, lse, pages, slots, max_pages,
                                 page_size, B, H, Hkv, nq, d, scale, window_left, window_right, n_sink,
                                 workspace, ws_bytes, stream)
+
+
+def attn_pages_reserve(table, lens, refs, seqs, counts, start, pages, slots, max_pages, page_size, n,
+                       stream) -> int:
+    return _lib.attn_pages_reserve(table, lens, refs, seqs, counts, start, pages, slots, max_pages,
+                                   page_size, n, stream)
+
+
+def attn_pages_fork(table, lens, refs, src, dst, from_, to, pages, slots, max_pages, page_size, n,
+                    stream) -> int:
+    return _lib.attn_pages_fork(table, lens, refs, src, dst, from_, to, pages, slots, max_pages,
+                                page_size, n, stream)
+
+
+def attn_pages_free(table, lens, refs, seqs, pages, slots, max_pages, page_size, n, window_left, n_sink,
+                    stream) -> int:
+    return _lib.attn_pages_free(table, lens, refs, seqs, pages, slots, max_pages, page_size, n,
+                                window_left, n_sink, stream)
+
+
+def attn_pages_workspace_bytes(pages) -> int:
+    return _lib.attn_pages_workspace_bytes(pages)
+
+
+def attn_pages_compact(table, refs, from_, to, count, pages, slots, max_pages, workspace, ws_bytes,
+                       stream) -> int:
+    return _lib.attn_pages_compact(table, refs, from_, to, count, pages, slots, max_pages, workspace,
+                                   ws_bytes, stream)
+
+
+def attn_pages_copy(pool, from_, to, count, layers, pages, page_bytes, n, stream) -> int:
+    return _lib.attn_pages_copy(pool, from_, to, count, layers, pages, page_bytes, n, stream)
 
 
 # ---------------------------------------------------------------- torch-tensor wrappers
@@ -206,3 +260,106 @@ def kv4_attend(q, pool, table, lens, window=None, sinks=0, scale=None, seqs=None
     if rc:
         raise AttnError(rc, "attn_kv4_attend")
     return out, lse
+
+
+def _page_state(where, table, lens, refs, *ts):
+    """Checks the state and the int32 vectors of one call; (pages, slots, max_pages, device)."""
+    _is(where, "table", table, torch.int32, None, None)
+    slots, width = table.shape
+    if lens is not None:
+        _is(where, "lens", lens, torch.int32, slots)
+    _is(where, "refs", refs, torch.int32, None)
+    for t in ts:
+        _is(where, "rows and counts", t, torch.int32, ts[0].shape[0])
+    return refs.shape[0], slots, width, _tensors(where, table, lens, refs, *ts)
+
+
+def pages_reserve(table, lens, refs, page_size, seqs, counts, stream=None):
+    """Sequences seqs[i] grow by counts[i] tokens: pages are taken for them and lens follows. Returns
+    start (n,), the first new token of each (its length before), or -1 throughout if the call was
+    refused: pages or table columns ran out, or a row is out of range or given twice."""
+    where = "pages_reserve"
+    pages, slots, width, dev = _page_state(where, table, lens, refs, seqs, counts)
+    start = torch.empty_like(seqs)
+    rc = _lib.attn_pages_reserve(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), seqs.data_ptr(),
+                                 counts.data_ptr(), start.data_ptr(), pages, slots, width, page_size,
+                                 seqs.shape[0], _raw_stream(stream, dev, start))
+    if rc:
+        raise AttnError(rc, "attn_pages_reserve")
+    return start
+
+
+def pages_fork(table, lens, refs, page_size, src, dst, stream=None):
+    """The empty sequences dst[i] become src[i] and share its full pages; a partly filled last page gets
+    a page of its own. Returns (from, to) (n,) int32 for `pages_copy`, -1 where there is nothing to copy
+    or the call was refused (pages ran out, a dst not empty, given twice or also a src)."""
+    where = "pages_fork"
+    pages, slots, width, dev = _page_state(where, table, lens, refs, src, dst)
+    frm, to = torch.empty_like(src), torch.empty_like(src)
+    rc = _lib.attn_pages_fork(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), src.data_ptr(),
+                              dst.data_ptr(), frm.data_ptr(), to.data_ptr(), pages, slots, width, page_size,
+                              src.shape[0], _raw_stream(stream, dev, frm, to))
+    if rc:
+        raise AttnError(rc, "attn_pages_fork")
+    return frm, to
+
+
+def pages_free(table, lens, refs, page_size, seqs, window=None, sinks=0, stream=None):
+    """Without a window the sequences end: their pages lose a reference, their rows and lengths are
+    cleared. With window=(left, right) only pages are given back whose tokens no query from the next
+    token on sees under that window and these sinks; their entries become -1."""
+    where = "pages_free"
+    pages, slots, width, dev = _page_state(where, table, lens, refs, seqs)
+    sinks = _sinks(sinks)
+    left = -1 if window is None else int(window[0])
+    if window is not None and left < 0:
+        return                                  # an open window: every token stays visible
+    rc = _lib.attn_pages_free(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), seqs.data_ptr(), pages,
+                              slots, width, page_size, seqs.shape[0], left, sinks,
+                              _raw_stream(stream, dev))
+    if rc:
+        raise AttnError(rc, "attn_pages_free")
+
+
+def pages_compact(table, refs, workspace=None, stream=None):
+    """Renumbers the pages in use to 0 .. L-1. Returns (from, to, count) for `pages_copy`: page from[r]
+    becomes to[r] for r < count[0], -1 behind."""
+    where = "pages_compact"
+    pages, slots, width, dev = _page_state(where, table, None, refs)
+    if workspace is not None:
+        _tensors(where, workspace)
+    need = (pages + 4) * 4
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=refs.device)
+    half = max(pages // 2, 1)
+    out = torch.empty(2 * half + 1, dtype=torch.int32, device=refs.device)
+    frm, to, count = out[:half], out[half:2 * half], out[2 * half:]
+    rc = _lib.attn_pages_compact(table.data_ptr(), refs.data_ptr(), frm.data_ptr(), to.data_ptr(),
+                                 count.data_ptr(), pages, slots, width, workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(),
+                                 _raw_stream(stream, dev, out, workspace))
+    if rc:
+        raise AttnError(rc, "attn_pages_compact")
+    return frm, to, count
+
+
+def pages_copy(pool, frm, to, count=None, layered=False, stream=None):
+    """Copies the contents of page frm[i] to page to[i] for i < count[0] (all, without count); pairs with
+    a number outside the pool are skipped. pool: (pages, ...) of any type, or (layers, pages, ...) with
+    layered=True (the same pages of every layer). No page may be both copied from and to."""
+    where = "pages_copy"
+    if pool.dim() < (2 if layered else 1):
+        raise ValueError(f"{where}: the pool needs a dimension of pages")
+    _is(where, "frm", frm, torch.int32, None)
+    _is(where, "to", to, torch.int32, frm.shape[0])
+    if count is not None:
+        _is(where, "count", count, torch.int32, 1)
+    dev = _tensors(where, pool, frm, to, count)
+    layers, pages = (pool.shape[0], pool.shape[1]) if layered else (1, pool.shape[0])
+    if layers < 1 or pages < 1:
+        raise ValueError(f"{where}: the pool is empty")
+    each = pool.numel() // (layers * pages) * pool.element_size()
+    rc = _lib.attn_pages_copy(pool.data_ptr(), frm.data_ptr(), to.data_ptr(), _at(count), layers, pages, each,
+                              frm.shape[0], _raw_stream(stream, dev))
+    if rc:
+        raise AttnError(rc, "attn_pages_copy")

@@ -37,7 +37,10 @@
  *   ATTN_ERR_WORKSPACE    ws_bytes smaller than attn_bwd_workspace_bytes();
  *   ATTN_ERR_CUDA      a launch or encode error reported by the CUDA runtime / driver;
  *   ATTN_ERR_TIMEOUT   reported by attn_get_device_status(): a device-side wait ran past its
- *                      limit and the kernel returned early (outputs are then undefined).
+ *                      limit and the kernel returned early (outputs are then undefined);
+ *   ATTN_ERR_PAGES     reported by attn_get_device_status(): an attn_pages_* call was refused on the
+ *                      device (too few free pages, an index out of range or given twice) and
+ *                      changed nothing.
  */
 #ifndef ATTN_H
 #define ATTN_H
@@ -56,7 +59,8 @@ enum {
     ATTN_ERR_UNSUPPORTED = 2,
     ATTN_ERR_CUDA = 3,
     ATTN_ERR_TIMEOUT = 4,
-    ATTN_ERR_WORKSPACE = 5
+    ATTN_ERR_WORKSPACE = 5,
+    ATTN_ERR_PAGES = 6
 };
 
 /* Library ABI version (major*100 + minor). */
@@ -352,6 +356,48 @@ int attn_kv4_attend(const void* q, const void* pool, const int* table, const int
                     int page_size, int B, int H, int Hkv, int nq, int d, float scale,
                     int window_left, int window_right, int n_sink, void* workspace, size_t ws_bytes,
                     void* stream);
+
+/* Pages of a K/V cache. State, in caller-owned device memory, int32: table (slots, max_pages), the
+ * pages of each sequence's tokens in order, -1: none; lens (slots), its tokens; refs (pages; 16-byte
+ * aligned), how many table entries name a page. A page with refs 0 is free; an empty sequence has
+ * lens 0 and a row of -1. The state is read and changed on the device, in stream order, without
+ * synchronising; calls on one state must be ordered. Contents move only by attn_pages_copy, once for
+ * every pool that the table serves. Free pages are taken from the lowest number up, in the order of
+ * the entries. A call that cannot be served as a whole changes nothing: start, from and to are -1 and
+ * the device status becomes ATTN_ERR_PAGES.
+ *
+ * attn_pages_reserve: sequences seqs[i] grow by counts[i] >= 0 tokens; start[i] = its length before, the
+ *   first new token (for attn_kv4_append, which leaves out entries with a negative start). Refused
+ *   when pages or table columns run out, or a row is out of range or given twice.
+ * attn_pages_fork: the empty sequence dst[i] becomes src[i]: it shares the full pages, and a partly
+ *   filled last page is given a page of its own, whose contents the caller copies from from[i] to to[i]
+ *   (-1: nothing to copy). One src may be forked many times. Refused when pages run out, a dst is not
+ *   empty, given twice or also a src, or a row is out of range.
+ * attn_pages_free: window_left < 0: the sequences end (lens 0, row -1). window_left >= 0: only pages
+ *   whose tokens no query from the next token on sees under that window and n_sink sinks are given
+ *   back; their entries become -1. Rows out of range are skipped (and reported); a row given twice
+ *   counts once. n >= 1 rows.
+ * attn_pages_compact: the L pages in use move to the numbers below L: from[r] -> to[r] for r < *count,
+ *   both ascending, -1 behind; from and to hold max(pages / 2, 1) entries. Table and refs follow.
+ *   Workspace: attn_pages_workspace_bytes(pages), 16-byte aligned.
+ * attn_pages_copy: contents of page from[i] to page to[i], i < min(n, *count) (count NULL: n), in each
+ *   of `layers` pools of `pages` pages of page_bytes bytes that follow one another. Pairs with a number
+ *   outside [0, pages) are skipped; no page may be both copied from and to.
+ * n <= 8192 sequences for reserve and fork, slots <= 262144; other sizes below 1, null or misaligned
+ * pointers, max_pages·page_size > 2^31 - 257, page_bytes no multiple of 16 -> ATTN_ERR_INVALID. */
+int attn_pages_reserve(int* table, int* lens, int* refs, const int* seqs, const int* counts,
+                       int* start, int pages, int slots, int max_pages, int page_size, int n,
+                       void* stream);
+int attn_pages_fork(int* table, int* lens, int* refs, const int* src, const int* dst, int* from,
+                    int* to, int pages, int slots, int max_pages, int page_size, int n,
+                    void* stream);
+int attn_pages_free(int* table, int* lens, int* refs, const int* seqs, int pages, int slots,
+                    int max_pages, int page_size, int n, int window_left, int n_sink, void* stream);
+size_t attn_pages_workspace_bytes(int pages);
+int attn_pages_compact(int* table, int* refs, int* from, int* to, int* count, int pages, int slots,
+                       int max_pages, void* workspace, size_t ws_bytes, void* stream);
+int attn_pages_copy(void* pool, const int* from, const int* to, const int* count, int layers,
+                    int pages, long long page_bytes, int n, void* stream);
 
 /* Measurement hook. `events` is NULL (recording off, the default) or an array of 4 cudaEvent_t
  * created by the caller. While set, every attn_bwd call records, on its stream, events[0] before
