@@ -3,6 +3,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 #include "kv4.h"
 #include "sm100_ptx.cuh"
@@ -206,12 +208,12 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4RowsAr
 // All query rows of one K/V head (its query heads times nq tokens) share every byte that is read,
 // so a (batch entry, K/V head, block of 8·NT rows) is one segment of work, its keys the blocks of
 // 16 tokens that any row sees: those of the sinks, then those of the window. The segments' tiles
-// (4 blocks) laid end to end are cut into equal runs, one per CTA, whatever the lengths of the
+// (8 blocks, or 4) laid end to end are cut into equal runs, one per CTA, whatever the lengths of the
 // sequences; a CTA writes the segments it holds whole and leaves the parts of the others in
 // the workspace, where a second launch joins them with the rule that joins two softmax blocks.
 //
-// Each of a CTA's 4 warps takes every fourth block through a ring of its own (bulk copies
-// of a whole block, contiguous in memory, one mbarrier per stage): no barrier among the warps until a
+// Each of a CTA's 4 warps takes its blocks of a tile through a ring of its own (bulk copies
+// of whole blocks, contiguous in memory, one mbarrier per stage): no barrier among the warps until a
 // segment ends. The two products run as mma.m16n8k16 (fp16 in, fp32 sums); tcgen05's smallest tile
 // of 128 rows would be filled to 1/16 to 1/128 by the 1 to 8 rows there are, and its operands would
 // first have to be unpacked into shared memory.
@@ -236,12 +238,17 @@ struct AttCfg {
     static constexpr int G = D / 32;
     static constexpr int BB = kv4_block_bytes(D);
     static constexpr int ROWS = 8 * NT;
-    static constexpr int STAGES = D == 128 ? 3 : (D == 64 ? 5 : 8);
-    static constexpr int CTAS = NT == 1 ? 4 : 2;                        // per SM
-    static constexpr int RING = kAttWarps * STAGES * BB;
+    static constexpr int BL = NT == 1 ? 2 : 1;                          // blocks a warp takes per step
+    static constexpr int TILE = kAttWarps * BL;                         // blocks per tile
+    static constexpr int SB = BL * BB;                                  // bytes per stage
+    static constexpr int STAGES = NT == 1 ? (D == 128 ? 3 : (D == 64 ? 4 : 6)) : (D == 128 ? 4 : 8);
+    static constexpr int CTAS = NT == 1 ? (D == 128 ? 3 : 4) : 2;       // per SM
+    static constexpr int RING = kAttWarps * STAGES * SB;
     static constexpr int OPAD = D + 4;
-    static constexpr int MERGE = kAttWarps * ROWS * (OPAD + 2) * 4;     // O rows, then (m, l)
-    static constexpr int SMEM = RING + MERGE + kAttWarps * STAGES * 8 + 128;
+    static constexpr int SLOT = ROWS * (OPAD + 2);                      // floats: O rows, then (m, l)
+    static constexpr int MERGE = 2 * SLOT * 4;
+    static constexpr int QFRAG = NT * G * 32 * 16;                      // Q's fragments
+    static constexpr int SMEM = RING + MERGE + QFRAG + kAttWarps * STAGES * 8 + 512;   // and AttShared
     static constexpr int PART = ROWS * (D + 2);                         // floats of a part
 };
 
@@ -284,43 +291,79 @@ __device__ __forceinline__ AttSeq att_seq(const Kv4AttendArgs& a, int b) {
     return s;
 }
 
-__device__ __forceinline__ int att_tiles(const Kv4AttendArgs& a, int b) {
-    return (att_seq(a, b).nb + kAttWarps - 1) / kAttWarps;
-}
+__device__ __forceinline__ int att_tiles(const AttSeq& s, int tile) { return (s.nb + tile - 1) / tile; }
 
-// Sum of att_tiles over [0, n) (all threads of the CTA get it; `scratch` of kAttWarps long longs).
-__device__ __forceinline__ long long att_prefix(const Kv4AttendArgs& a, int n, int threads,
-                                                long long* scratch) {
-    long long t = 0;
-    for (int b = threadIdx.x; b < n; b += threads) t += att_tiles(a, b);
+// Sum of v over the CTA's threads below this one, and over all of them (`scratch`: one per warp).
+__device__ __forceinline__ long long att_scan(long long v, long long* all, long long* scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long incl = v;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = t;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) scratch[warp] = incl;
     __syncthreads();
-    t = 0;
-    for (int w = 0; w < threads / 32; ++w) t += scratch[w];
+    long long before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kAttWarps; ++w) {
+        if (w < warp) before += scratch[w];
+        sum += scratch[w];
+    }
     __syncthreads();
-    return t;
+    *all = sum;
+    return before + incl - v;
 }
 
-// Runs that `total` tiles are cut into: one per CTA, none shorter than 2 tiles.
+// Runs that `total` tiles are cut into (one per CTA), and the first tile of run k. Almost always
+// 32 bits do: a 64-bit division takes ten times as long, and every CTA waits for it.
 __host__ __device__ inline long long att_runs(long long total, int ctas) {
-    const long long r = (total + 1) / 2;
-    return r < ctas ? r : ctas;
+    return total < ctas ? total : ctas;
+}
+__device__ __forceinline__ long long att_run_start(long long total, int k, long long runs) {
+    if (total < (1LL << 22)) return static_cast<unsigned>(total) * static_cast<unsigned>(k) / static_cast<unsigned>(runs);
+    return total * k / runs;
+}
+// Run that holds tile x: the last k with total·k / runs <= x.
+__device__ __forceinline__ int att_run_of(long long x, long long total, long long runs) {
+    long long k = total < (1LL << 22) ? static_cast<unsigned>(x) * static_cast<unsigned>(runs) / static_cast<unsigned>(total)
+                                      : x * runs / total;
+    while (k + 1 < runs && att_run_start(total, static_cast<int>(k) + 1, runs) <= x) ++k;
+    return static_cast<int>(k);
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+// D = A·B + C, fp16 operands.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1, const float (&c)[4]) {
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+          "f"(c[3]));
+}
+
+// D = A·B + C, bf16 operands, 8 or 16 along the sum.
+template <bool K16>
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1,
+                                         const float (&c)[4]) {
+    if constexpr (K16)
+        asm(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%4,%5}, {%6,%7}, "
+            "{%8,%9,%10,%11};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+    else
+        asm(
+            "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+            "{%7,%8,%9,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(b0), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -343,150 +386,208 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[G], const uint8_t* p) {
     }
 }
 
+// A run's place: batch entry, (K/V head, row block), the tiles [t0, t1) of that segment that the run
+// holds, and the run's tiles before them.
+struct AttPart {
+    AttSeq seq;
+    int b, hr, t0, t1;
+    long long x;
+};
+
+struct AttShared {
+    long long scratch[kAttWarps];
+    AttPart part, fetch[kAttWarps];     // the computation's place, and each warp's fetching
+    int abort, more;
+};
+static_assert(sizeof(AttShared) <= 512, "shared block");
+
+// Clips the part to the run's end, or moves on to the next segment (false: the run is over).
+template <int TILE>
+__device__ __forceinline__ void att_clip(AttPart& q, long long x1) {
+    q.t1 = static_cast<int>(min(static_cast<long long>(att_tiles(q.seq, TILE)), q.t0 + (x1 - q.x)));
+}
+template <int TILE>
+__device__ __forceinline__ bool att_next(const Kv4AttendArgs& a, AttPart& q, int HR, long long x1) {
+    q.x += q.t1 - q.t0;
+    if (q.x >= x1) return false;
+    q.t0 = 0;
+    if (++q.hr == HR) {
+        q.hr = 0;
+        do {
+            if (++q.b >= a.B) return false;            // only if lens changed under the call
+            q.seq = att_seq(a, q.b);
+        } while (q.seq.nb == 0);
+    }
+    att_clip<TILE>(q, x1);
+    return true;
+}
+
+// Steps of warp w in the part: its blocks begin at list positions TILE·t + BL·w below nb.
+template <int TILE, int BL>
+__device__ __forceinline__ int att_steps(const AttPart& q, int w) {
+    const int rest = q.seq.nb - 1 - BL * w;
+    const int last = rest >= 0 ? rest / TILE : -1;             // its last tile
+    return max(min(q.t1, last + 1) - q.t0, 0);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_kernel(const AttParams p) {
     using C = AttCfg<D, NT>;
     constexpr int G = C::G, ST = C::STAGES;
     extern __shared__ __align__(1024) uint8_t smem[];
     float* merge = reinterpret_cast<float*>(smem + C::RING);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING + C::MERGE);
-    long long* scratch = reinterpret_cast<long long*>(bars + kAttWarps * ST);
-    int* abort_s = reinterpret_cast<int*>(scratch + kAttWarps);
-    volatile int* abort = abort_s;
+    uint4* qfrag = reinterpret_cast<uint4*>(smem + C::RING + C::MERGE);   // [NT][G][lane]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING + C::MERGE + C::QFRAG);
+    AttShared* sh = reinterpret_cast<AttShared*>(bars + kAttWarps * ST);
+    volatile int* abort = &sh->abort;
     const Kv4AttendArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, c = lane & 3;
-    uint8_t* ring = smem + warp * ST * C::BB;
+    uint8_t* ring = smem + warp * ST * C::SB;
     uint64_t* full = bars + warp * ST;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kAttWarps * ST; ++s) mbar_init(&bars[s], 1);
-        *abort_s = 0;
+        sh->abort = 0;
+        sh->part.b = -1;
         fence_barrier_init();
     }
-    // ---- this CTA's run of tiles, and the segment it begins in (att_prefix synchronises the CTA)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");    // the joining launch may be set up
+    // ---- this CTA's run of tiles, and the segment it begins in
     const int HR = a.pool.Hkv * p.RB;
-    const long long per_head = att_prefix(a, a.B, kAttThreads, scratch);
-    const long long total = per_head * HR;
-    const long long runs = att_runs(total, gridDim.x);
-    if (blockIdx.x >= runs) return;
-    const long long x0 = total * blockIdx.x / runs, x1 = total * (blockIdx.x + 1) / runs;
-    int b = 0, hr;
-    long long tile;       // in the segment
+    long long x0, x1;
     {
-        // batch entry of tile x0: entries hold HR segments of att_tiles(b) tiles each
-        long long before = 0;
-        while (true) {    // b advances by whole chunks of threads, then by the prefix within one
-            const int bb = b + static_cast<int>(threadIdx.x);
-            long long t = bb < a.B ? static_cast<long long>(att_tiles(a, bb)) * HR : 0, incl = t;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            if (lane == 31) scratch[warp] = incl;
-            __syncthreads();
-            long long chunk = 0, mine = before;
-            for (int w = 0; w < kAttWarps; ++w) {
-                if (w < warp) mine += scratch[w];
-                chunk += scratch[w];
-            }
-            __syncthreads();
-            if (x0 >= before + chunk) {
-                before += chunk;
-                b += kAttThreads;
-                if (b >= a.B) return;      // only if lens changed under the call
-                continue;
-            }
-            mine += incl - t;                              // tiles before entry bb
-            if (x0 >= mine && x0 < mine + t) {
-                scratch[0] = bb;
-                scratch[1] = x0 - mine;
-            }
-            __syncthreads();
-            b = static_cast<int>(scratch[0]);
-            tile = scratch[1];
-            __syncthreads();
-            break;
+        // a thread per batch entry; the one that holds the run's first tile writes down the place.
+        // More entries than threads: chunks of them, once for the total and once for the place
+        long long total = 0, before = 0;
+        AttSeq mine{};
+        for (int b0 = 0; b0 < a.B; b0 += kAttThreads) {
+            const int b = b0 + static_cast<int>(threadIdx.x);
+            mine.nb = 0;
+            if (b < a.B) mine = att_seq(a, b);
+            long long all;
+            before = total + att_scan(att_tiles(mine, C::TILE), &all, sh->scratch);
+            total += all;
         }
+        total *= HR;
+        const long long runs = att_runs(total, gridDim.x);
+        if (blockIdx.x >= runs) return;
+        x0 = att_run_start(total, blockIdx.x, runs);
+        x1 = att_run_start(total, blockIdx.x + 1, runs);
+        long long chunk = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kAttThreads) {
+            const int b = b0 + static_cast<int>(threadIdx.x);
+            if (a.B > kAttThreads) {
+                mine.nb = 0;
+                if (b < a.B) mine = att_seq(a, b);
+                long long all;
+                before = chunk + att_scan(att_tiles(mine, C::TILE), &all, sh->scratch);
+                chunk += all;
+            }
+            const int nt = att_tiles(mine, C::TILE);
+            if (nt > 0 && x0 >= before * HR && x0 < (before + nt) * HR) {
+                AttPart q;
+                const long long tile = x0 - before * HR;
+                q.seq = mine;
+                q.b = b;
+                q.x = x0;
+                q.hr = static_cast<int>(tile < (1LL << 31) ? static_cast<unsigned>(tile) / static_cast<unsigned>(nt)
+                                                           : tile / nt);
+                q.t0 = static_cast<int>(tile - static_cast<long long>(q.hr) * nt);
+                att_clip<C::TILE>(q, x1);
+                sh->part = q;
+                for (int w = 0; w < kAttWarps; ++w) sh->fetch[w] = q;
+            }
+        }
+        __syncthreads();
+        if (sh->part.b < 0) return;        // only if lens changed under the call
     }
-    AttSeq seq = att_seq(a, b);
-    if (seq.nb == 0) return;               // (as above: the loops below count on what they read)
-    {
-        const int nt = (seq.nb + kAttWarps - 1) / kAttWarps;
-        hr = static_cast<int>(tile / nt);
-        tile -= static_cast<long long>(hr) * nt;
-    }
+    const AttPart& q = sh->part;
     const int bpp = a.pool.page_size / kKv4Block;
+    const int step_pages = C::TILE / bpp, step_blocks = C::TILE % bpp;    // one tile on
     const uint64_t lim = a.timeout_ns;
 
-    // ---- fetching: a cursor over the run's tiles, ST blocks ahead of the one over the computation
-    AttSeq fs = seq;
-    int fb = b, fhr = hr, ft = static_cast<int>(tile);
-    long long fx = x0;
-    int pid = -1, fblk = 0, fhead = 0;      // page of the next block to fetch (loaded ahead of its use)
+    // ---- fetching: its own place in the run, ST steps ahead of the computation's. Lane i < BL holds
+    // block i of the warp's next step: block f_blk of page column f_col, the page's number loaded one
+    // step ahead of its use; `left` steps remain in the place's part.
+    AttPart& f = sh->fetch[warp];
+    int left = 0, f_li = 0, f_sb = 0, f_nb = 0, f_col = 0, f_blk = 0, n_blk = 0, pid = -1;
+    const int* row = nullptr;              // the sequence's row of the table
+    const uint8_t* heads = nullptr;        // page 0's blocks of the part's head
     bool more = true;
-    // moves the cursor to this warp's next block and starts loading its page number
-    auto seek = [&]() {
-        while (fx < x1) {
-            const int li = ft * kAttWarps + warp;
-            const bool have = li < fs.nb;
-            if (have) {
-                const int tb = li < fs.sb ? li : fs.wb0 + li - fs.sb;
-                fblk = tb % bpp;
-                fhead = fhr / p.RB;
-                pid = a.pool.table[static_cast<size_t>(fs.slot) * a.pool.max_pages + tb / bpp];
-            }
-            ++fx;
-            if (++ft * kAttWarps >= fs.nb) {
-                ft = 0;
-                if (++fhr == HR) {
-                    fhr = 0;
-                    if (fx < x1)
-                        do fs = att_seq(a, ++fb);
-                        while (fs.nb == 0 && fb + 1 < a.B);
-                }
-            }
-            if (have) return;
-        }
-        more = false;
+    const size_t page_bytes = static_cast<size_t>(a.pool.Hkv) * bpp * C::BB;
+    auto place = [&]() {                   // column and block of list position f_li
+        const int tb = f_li < f_sb ? f_li : f.seq.wb0 + f_li - f_sb;
+        f_col = tb / bpp;
+        f_blk = tb - f_col * bpp;
     };
-    uint32_t valid = 0;                     // stages that hold a block (not a page that is missing)
-    int issued = 0, taken = 0;              // blocks
+    auto open = [&]() {
+        left = att_steps<C::TILE, C::BL>(f, warp);
+        f_li = f.t0 * C::TILE + warp * C::BL + lane;
+        f_sb = f.seq.sb;
+        f_nb = lane < C::BL ? f.seq.nb : 0;
+        place();
+        row = a.pool.table + static_cast<size_t>(f.seq.slot) * a.pool.max_pages;
+        heads = a.pool.data + static_cast<size_t>(f.hr / p.RB) * bpp * C::BB;
+    };
+    auto look = [&]() {                    // starts loading the page numbers of the next step
+        while (left == 0) {
+            __syncwarp();
+            int go = 0;
+            if (lane == 0) go = att_next<C::TILE>(a, f, HR, x1);
+            go = __shfl_sync(0xffffffffu, go, 0);
+            __syncwarp();
+            if (!go) {
+                more = false;
+                return;
+            }
+            open();
+        }
+        pid = f_li < f_nb ? row[f_col] : -1;
+        n_blk = f_blk;
+        --left;
+        const bool in_sinks = f_li < f_sb;
+        f_li += C::TILE;
+        f_col += step_pages;
+        f_blk += step_blocks;
+        if (f_blk >= bpp) {
+            f_blk -= bpp;
+            ++f_col;
+        }
+        if (in_sinks && f_li >= f_sb) place();
+    };
+    uint32_t valid = 0;                    // BL bits per stage: blocks on a page
+    int issued = 0, taken = 0, fs = 0, cs = 0;             // steps, and their stages
+    uint32_t phase = 0;
     auto fetch = [&]() {
         if (!more) return;
-        const int s = issued % ST;
-        const bool ok = pid >= 0 && pid < a.pool.pages;
-        valid = ok ? valid | (1u << s) : valid & ~(1u << s);
-        if (lane == 0) {
-            if (ok) {
-                const uint8_t* src =
-                    a.pool.data + ((static_cast<size_t>(pid) * a.pool.Hkv + fhead) * bpp + fblk) * C::BB;
-                mbar_arrive_expect_tx(&full[s], C::BB);
-                bulk_load(ring + s * C::BB, src, C::BB, &full[s]);
-            } else {
-                mbar_arrive(&full[s]);
-            }
-        }
+        const bool held = static_cast<unsigned>(pid) < static_cast<unsigned>(a.pool.pages);
+        const uint32_t bits = __ballot_sync(0xffffffffu, held);
+        valid = (valid & ~(((1u << C::BL) - 1u) << (fs * C::BL))) | bits << (fs * C::BL);
+        if (lane == 0) mbar_arrive_expect_tx(&full[fs], __popc(bits) * C::BB);
+        __syncwarp();
+        if (held)
+            bulk_load(ring + fs * C::SB + lane * C::BB,
+                      heads + static_cast<size_t>(pid) * page_bytes + static_cast<size_t>(n_blk) * C::BB, C::BB,
+                      &full[fs]);
         ++issued;
-        seek();
+        fs = fs + 1 == ST ? 0 : fs + 1;
+        look();
     };
-    seek();
+    open();
+    look();
     for (int s = 0; s < ST; ++s) fetch();
 
-    long long x = x0;
     bool ok = true;
-    while (x < x1) {
+    while (true) {
         // ---- one segment's part of the run
-        const int nt_all = (seq.nb + kAttWarps - 1) / kAttWarps;
-        const int t0 = static_cast<int>(tile);
-        const int t1 = static_cast<int>(min(static_cast<long long>(nt_all), tile + (x1 - x)));
-        const int head = hr / p.RB, row0 = hr % p.RB * C::ROWS;
-        const size_t qbase = (static_cast<size_t>(b) * a.pool.Hkv + head) * p.R;
-        // Q as the B operand of S: lane (gid, c) holds row gid, channels 32·g + 8·c .. + 7
-        uint32_t qf[NT][G][4];
-        float qsum[NT][G][2];       // scale·log2(e)·sum over the group, of rows 2c, 2c + 1
+        const int head = q.hr / p.RB, row0 = q.hr % p.RB * C::ROWS;
+        const size_t qbase = (static_cast<size_t>(q.b) * a.pool.Hkv + head) * p.R;
+        // Q as the B operand of S: lane (gid, c) holds row gid, channels 32·g + 8·c .. + 7. qs is the
+        // B operand that meets the keys' lo: scale·log2(e)·(sum over each group) in three bf16 parts
+        // (Q lies in shared memory: the 4 warps read the same fragments, and 16 registers fewer let four
+        // CTAs stay on an SM)
+        uint32_t qs[NT][2];
         float cq[NT][2];            // scale·log2(e)·2^24 / (Q's power of two), of rows 2c, 2c + 1
-        int pos[NT][2];             // key position of those rows, relative to off
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = row0 + n * 8 + gid;
@@ -507,44 +608,75 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
                 }
                 sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
                 sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+                sum[g] *= p.scale_log2;
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             // amax in 2^(e-127) .. 2^(e-126): times 2^(141-e) it lies in 2^14 .. 2^15
             const int up = min(141 - static_cast<int>(__float_as_uint(amax) >> 23), 127);
-            const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+            const float fq = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const uint32_t u[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+                uint32_t qf[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float m = (e & 1) ? f * 0.0625f : f;
-                    qf[n][g][e] = pack_f16x2(__uint_as_float(u[e] << 16) * m,
-                                             __uint_as_float(u[e] & 0xffff0000u) * m);
+                    const float m = (e & 1) ? fq * 0.0625f : fq;
+                    qf[e] = pack_f16x2(__uint_as_float(u[e] << 16) * m,
+                                       __uint_as_float(u[e] & 0xffff0000u) * m);
                 }
+                if (warp == 0) qfrag[(n * G + g) * 32 + lane] = make_uint4(qf[0], qf[1], qf[2], qf[3]);
             }
             const float back = ldexpf(p.scale_log2, 24 - up);
+            cq[n][0] = __shfl_sync(0xffffffffu, back, 8 * c);
+            cq[n][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+            // sums x = hi + mid + low. Along the sum, lane c holds: d = 128 the groups 2·(c & 1) and the
+            // next, hi in c < 2, mid in c >= 2, low in c < 2 of the second half; d = 64 both groups,
+            // part c; d = 32 (hi, mid) in c = 0, low in c = 1
+            uint32_t part[3];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int src = (2 * c + e) * 4;
-                cq[n][e] = __shfl_sync(0xffffffffu, back, src);
+            for (int t = 0; t < 3; ++t) {
+                const float s0 = G == 4 ? ((c & 1) ? sum[G / 2] : sum[0]) : sum[0];
+                const float s1 = G == 4 ? ((c & 1) ? sum[G - 1] : sum[G / 4]) : sum[G - 1];
+                float h0 = s0, h1 = s1, b0 = 0.f, b1 = 0.f;
 #pragma unroll
-                for (int g = 0; g < G; ++g)
-                    qsum[n][g][e] = __shfl_sync(0xffffffffu, sum[g], src) * p.scale_log2;
-                pos[n][e] = (row0 + n * 8 + 2 * c + e) % a.nq;
+                for (int k = 0; k <= t; ++k) {
+                    b0 = __bfloat162float(__float2bfloat16_rn(h0));
+                    b1 = __bfloat162float(__float2bfloat16_rn(h1));
+                    h0 -= b0;
+                    h1 -= b1;
+                }
+                part[t] = pack_bf16x2(b0, b1);
+            }
+            if constexpr (G == 4) {
+                qs[n][0] = c < 2 ? part[0] : part[1];
+                qs[n][1] = c < 2 ? part[2] : 0u;
+            } else if constexpr (G == 2) {
+                qs[n][0] = c == 0 ? part[0] : c == 1 ? part[1] : c == 2 ? part[2] : 0u;
+                qs[n][1] = 0u;
+            } else {
+                qs[n][0] = c == 0 ? (part[0] & 0xffffu) | (part[1] << 16) : c == 1 ? part[2] & 0xffffu : 0u;
+                qs[n][1] = 0u;
             }
         }
-        // blocks [full_lo, full_hi] (by first key) are seen whole by every row
-        const long long full_lo = a.wl < 0 ? 0 : seq.off + a.nq - 1 - a.wl;
-        const long long full_hi = (a.wr < 0 ? seq.last : min(seq.off + a.wr, static_cast<long long>(seq.last))) -
-                                  (kKv4Block - 1);
-        float m[NT][2], l[NT][2], ol[NT][G][2], acc[NT][2 * G][4];
-        float fv = 0x1p127f;        // power of two on P·s
+        __syncthreads();
+        // blocks [full_lo, full_hi], and those below full_ns, are seen whole by every row
+        const long long lo_key = a.wl < 0 ? 0 : q.seq.off + a.nq - 1 - a.wl;
+        const long long hi_key = a.wr < 0 ? q.seq.last : min(q.seq.off + a.wr, static_cast<long long>(q.seq.last));
+        const int full_lo = static_cast<int>(max(lo_key + kKv4Block - 1, 0LL) / kKv4Block);
+        const int full_hi = hi_key < kKv4Block - 1 ? -1 : static_cast<int>((hi_key + 1) / kKv4Block) - 1;
+        const int full_ns = a.ns / kKv4Block;
+        // nm = minus the running maximum (0 until a row has seen a key); a score moves it when its
+        // excess is above thr.
+        float nm[NT][2], thr[NT][2], acc[NT][2 * G][4];
+        float l[NT][2], ol[NT][G][2];
+        float fv = 0x1p118f;        // power of two on P·s (P <= 2^8, s is 0 or at least 2^-100)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                m[n][e] = -INFINITY;
+                nm[n][e] = 0.f;
+                thr[n][e] = -INFINITY;
                 l[n][e] = 0.f;
 #pragma unroll
                 for (int g = 0; g < G; ++g) ol[n][g][e] = 0.f;
@@ -554,262 +686,342 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[n][t][e] = 0.f;
         }
-        for (int t = t0; ok && t < t1; ++t) {
-            const int li = t * kAttWarps + warp;
-            if (li >= seq.nb) break;
-            const int st = taken % ST;
-            const bool held = valid >> st & 1u;
-            ok = bounded_wait_warp(&full[st], (taken / ST) & 1, abort, lim);
-            ++taken;
-            if (!ok) break;
-            if (held) {
-                const int tb = li < seq.sb ? li : seq.wb0 + li - seq.sb;
-                const long long k0 = static_cast<long long>(tb) * kKv4Block;
-                const bool edge = (k0 < full_lo && k0 + kKv4Block > a.ns) || k0 > full_hi;
-                const uint8_t* blk = ring + st * C::BB;
-                // parameters of keys gid and gid + 8
-                float ks[2][G], kl[2][G], vs[2][G], vl[2][G];
+        // One step: BL blocks of 16 keys at blk, token blocks tb[], those that are there in `on`. EDGE:
+        // some row does not see some key. Everything is done for all blocks before the next thing, so
+        // that their chains of dependent instructions overlap.
+        auto step = [&](const uint8_t* blk, const int (&tb)[C::BL], uint32_t on, auto edge) {
+            constexpr bool EDGE = decltype(edge)::value;
+            constexpr int BL = C::BL;
+            // ---- scores relative to the running maximum: t = S - m
+            float t[BL][NT][4];     // (key gid, rows 2c, 2c + 1), (key gid + 8, ...)
+            float zs[BL][NT][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[G];
-                    lds_words<G>(w, blk + 16 * D + (h * 8 + gid) * G * 4);
+            for (int x = 0; x < BL; ++x) {
+                const uint8_t* par = blk + x * C::BB + 16 * D;
+                uint32_t a0, a1;                 // the keys' lo as the A operand
+                if constexpr (G == 4) {
+                    const uint2 w0 = *reinterpret_cast<const uint2*>(par + gid * 16 + (c & 1) * 8);
+                    const uint2 w1 = *reinterpret_cast<const uint2*>(par + (8 + gid) * 16 + (c & 1) * 8);
+                    a0 = __byte_perm(w0.x, w0.y, 0x7632);
+                    a1 = __byte_perm(w1.x, w1.y, 0x7632);
+                } else {
+                    uint32_t w0[G], w1[G];
+                    lds_words<G>(w0, par + gid * G * 4);
+                    lds_words<G>(w1, par + (8 + gid) * G * 4);
+                    a0 = __byte_perm(w0[0], w0[G - 1], 0x7632);
+                    a1 = __byte_perm(w1[0], w1[G - 1], 0x7632);
+                }
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        ks[h][g] = __uint_as_float(w[g] << 16);
-                        kl[h][g] = __uint_as_float(w[g] & 0xffff0000u);
-                    }
-                    lds_words<G>(w, blk + 18 * D + (h * 8 + gid) * G * 4);
+                for (int n = 0; n < NT; ++n) {
+                    const float ref[4] = {nm[n][0], nm[n][1], nm[n][0], nm[n][1]};
+                    mma_bf16<G == 4>(t[x][n], a0, a1, qs[n][0], qs[n][1], ref);
+                }
+                uint32_t k0w[G], k1w[G], p0[G], p1[G];
+                lds_words<G>(k0w, blk + x * C::BB + lane * G * 4);
+                lds_words<G>(k1w, blk + x * C::BB + (32 + lane) * G * 4);
+                lds_words<G>(p0, par + gid * G * 4);
+                lds_words<G>(p1, par + (8 + gid) * G * 4);
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        vs[h][g] = __uint_as_float(w[g] << 16);
-                        vl[h][g] = __uint_as_float(w[g] & 0xffff0000u);
+                for (int g = 0; g < G; ++g) {
+                    const uint32_t y0 = k0w[g] >> 8, y1 = k1w[g] >> 8;
+                    const uint32_t a00 = k0w[g] & 0x000f000fu, a01 = k1w[g] & 0x000f000fu;
+                    const uint32_t a02 = k0w[g] & 0x00f000f0u, a03 = k1w[g] & 0x00f000f0u;
+                    const uint32_t a10 = y0 & 0x000f000fu, a11 = y1 & 0x000f000fu;
+                    const uint32_t a12 = y0 & 0x00f000f0u, a13 = y1 & 0x00f000f0u;
+                    const float s0 = __uint_as_float(p0[g] << 16), s1 = __uint_as_float(p1[g] << 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const uint4 qf = qfrag[(n * G + g) * 32 + lane];
+                        float s[4];
+                        mma_f16(s, a00, a01, a02, a03, qf.x, qf.y, zero);
+                        mma_f16(s, a10, a11, a12, a13, qf.z, qf.w, s);
+                        float(&z)[4] = zs[x][n];
+                        z[0] = g == 0 ? s[0] * s0 : fmaf(s[0], s0, z[0]);
+                        z[1] = g == 0 ? s[1] * s0 : fmaf(s[1], s0, z[1]);
+                        z[2] = g == 0 ? s[2] * s1 : fmaf(s[2], s1, z[2]);
+                        z[3] = g == 0 ? s[3] * s1 : fmaf(s[3], s1, z[3]);
                     }
                 }
-                // ---- S
-                float z[NT][4];     // (key gid, rows 2c, 2c + 1), (key gid + 8, ...)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) z[n][e] = 0.f;
-                {
-                    uint32_t k0w[G], k1w[G];
-                    lds_words<G>(k0w, blk + lane * G * 4);
-                    lds_words<G>(k1w, blk + (32 + lane) * G * 4);
+                    for (int e = 0; e < 4; ++e) t[x][n][e] = fmaf(zs[x][n][e], cq[n][e & 1], t[x][n][e]);
+            }
+            // V's parameters of keys gid and gid + 8
+            float vs[BL][2][G], vl[BL][2][G], smax = 0.f;
+            uint32_t hidden[BL][NT];
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const uint32_t y0 = k0w[g] >> 8, y1 = k1w[g] >> 8;
-                        const uint32_t a00 = k0w[g] & 0x000f000fu, a01 = k1w[g] & 0x000f000fu;
-                        const uint32_t a02 = k0w[g] & 0x00f000f0u, a03 = k1w[g] & 0x00f000f0u;
-                        const uint32_t a10 = y0 & 0x000f000fu, a11 = y1 & 0x000f000fu;
-                        const uint32_t a12 = y0 & 0x00f000f0u, a13 = y1 & 0x00f000f0u;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            float s[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma_f16(s, a00, a01, a02, a03, qf[n][g][0], qf[n][g][1]);
-                            mma_f16(s, a10, a11, a12, a13, qf[n][g][2], qf[n][g][3]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                z[n][e] = fmaf(s[e] * cq[n][e & 1], ks[e >> 1][g],
-                                               fmaf(kl[e >> 1][g], qsum[n][g][e & 1], z[n][e]));
-                        }
-                    }
-                }
-                uint32_t hidden[NT];
-                if (edge) {
+            for (int x = 0; x < BL; ++x) {
+                uint32_t w0[G], w1[G];
+                lds_words<G>(w0, blk + x * C::BB + 18 * D + gid * G * 4);
+                lds_words<G>(w1, blk + x * C::BB + 18 * D + (8 + gid) * G * 4);
+                if constexpr (EDGE) {
                     // keys a row does not see; the parameters of keys that no row sees may be anything
+                    const long long k0 = static_cast<long long>(tb[x]) * kKv4Block + gid;
+                    const bool there = on >> x & 1u;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        hidden[n] = 0;
+                        hidden[x][n] = 0;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const long long key = k0 + gid + 8 * (e >> 1);
-                            const long long at = seq.off + pos[n][e & 1];
-                            const bool seen = key <= seq.last && (a.wr < 0 || key <= at + a.wr) &&
+                            const long long key = k0 + 8 * (e >> 1);
+                            const long long at = q.seq.off + (row0 + n * 8 + 2 * c + (e & 1)) % a.nq;
+                            const bool seen = there && key <= q.seq.last && (a.wr < 0 || key <= at + a.wr) &&
                                               (a.wl < 0 || key >= at - a.wl || key < a.ns);
                             if (!seen) {
-                                z[n][e] = -INFINITY;
-                                hidden[n] |= 1u << e;
+                                t[x][n][e] = -INFINITY;
+                                hidden[x][n] |= 1u << e;
                             }
                         }
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const long long key = k0 + gid + 8 * h;
-                        if (key > seq.last || (a.wl >= 0 && key < seq.off - a.wl && key >= a.ns)) {
+                        const long long key = k0 + 8 * h;
+                        if (!there || key > q.seq.last || (a.wl >= 0 && key < q.seq.off - a.wl && key >= a.ns)) {
 #pragma unroll
-                            for (int g = 0; g < G; ++g) vs[h][g] = vl[h][g] = 0.f;
+                            for (int g = 0; g < G; ++g) (h == 0 ? w0 : w1)[g] = 0;
                         }
                     }
-                }
-                // ---- the running maximum, and the power of two on P·s, move rarely
-                bool grow = false;
-                float smax = 0.f;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) grow |= fmaxf(z[n][e], z[n][2 + e]) > m[n][e] + 8.f;
-#pragma unroll
-                for (int g = 0; g < G; ++g) smax = fmaxf(smax, fmaxf(vs[0][g], vs[1][g]));
-                if (__any_sync(0xffffffffu, grow || smax * fv > 128.f)) {
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1)
-                        smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
-                    float ratio = 1.f;
-                    if (smax * fv > 128.f) {
-                        // smax < 2^(e-126): times 2^(131-e) below 2^5
-                        const int e = min(131 - static_cast<int>(__float_as_uint(smax) >> 23), 127);
-                        const float now = e < -126 ? 0x1p-126f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                        ratio = now / fv;
-                        fv = now;
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float t = fmaxf(z[n][e], z[n][2 + e]);
-#pragma unroll
-                            for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                            t = fmaxf(t, m[n][e]);
-                            const float al = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - t);
-                            m[n][e] = t;
-                            l[n][e] *= al;
-#pragma unroll
-                            for (int g = 0; g < G; ++g) ol[n][g][e] *= al;
-                            const float ar = al * ratio;
-#pragma unroll
-                            for (int q = 0; q < 2 * G; ++q) {
-                                acc[n][q][e] *= ar;
-                                acc[n][q][2 + e] *= ar;
-                            }
-                        }
-                }
-                // ---- P, and P·s in fp16 as the B operand of O^T
-                uint32_t v0w[G], v1w[G];
-                lds_words<G>(v0w, blk + 8 * D + lane * G * 4);
-                lds_words<G>(v1w, blk + 8 * D + (32 + lane) * G * 4);
-                float pr[NT][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
-                    const float m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-                    pr[n][0] = ex2_approx(z[n][0] - m0);
-                    pr[n][1] = ex2_approx(z[n][1] - m1);
-                    pr[n][2] = ex2_approx(z[n][2] - m0);
-                    pr[n][3] = ex2_approx(z[n][3] - m1);
-                    l[n][0] += pr[n][0] + pr[n][2];
-                    l[n][1] += pr[n][1] + pr[n][3];
                 }
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float f0 = vs[0][g] * fv, f1 = vs[1][g] * fv;
+                    vs[x][0][g] = __uint_as_float(w0[g] << 16);
+                    vs[x][1][g] = __uint_as_float(w1[g] << 16);
+                    vl[x][0][g] = __uint_as_float(w0[g] & 0xffff0000u);
+                    vl[x][1][g] = __uint_as_float(w1[g] & 0xffff0000u);
+                    smax = fmax3(smax, vs[x][0][g], vs[x][1][g]);
+                }
+            }
+            // ---- the running maximum, and the power of two on P·s, move rarely
+            float tmax[NT][2];
+            bool grow = smax * fv > 128.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    tmax[n][e] = fmaxf(t[0][n][e], t[0][n][2 + e]);
+#pragma unroll
+                    for (int x = 1; x < BL; ++x) tmax[n][e] = fmax3(tmax[n][e], t[x][n][e], t[x][n][2 + e]);
+                    grow |= tmax[n][e] > thr[n][e];
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1)
+                    smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
+                float ratio = 1.f;
+                if (smax * fv > 128.f) {
+                    // smax < 2^(e-126): times 2^(131-e) below 2^5
+                    const int e = max(min(131 - static_cast<int>(__float_as_uint(smax) >> 23), 118), -126);
+                    const float now = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                    ratio = now / fv;
+                    fv = now;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float d = tmax[n][e];
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, o));
+                        const bool up = d > thr[n][e];
+                        const float al = !up ? 1.f : thr[n][e] == -INFINITY ? 0.f : ex2_approx(-d);
+                        if (up) {
+                            nm[n][e] -= d;
+                            thr[n][e] = 8.f;
+#pragma unroll
+                            for (int x = 0; x < BL; ++x) {
+                                t[x][n][e] -= d;
+                                t[x][n][2 + e] -= d;
+                            }
+                        }
+                        l[n][e] *= al;
+#pragma unroll
+                        for (int g = 0; g < G; ++g) ol[n][g][e] *= al;
+                        const float ar = al * ratio;
+#pragma unroll
+                        for (int k = 0; k < 2 * G; ++k) {
+                            acc[n][k][e] *= ar;
+                            acc[n][k][2 + e] *= ar;
+                        }
+                    }
+            }
+            // ---- P, and P·s in fp16 as the B operand of O^T
+            float pr[BL][NT][4], pf[BL][NT][4];         // (key gid, rows 2c, 2c + 1), (key gid + 8, ...)
+#pragma unroll
+            for (int x = 0; x < BL; ++x)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        pr[x][n][e] = ex2_approx(t[x][n][e]);
+                        pf[x][n][e] = pr[x][n][e] * fv;
+                    }
+                    l[n][0] += pr[x][n][0] + pr[x][n][2];
+                    l[n][1] += pr[x][n][1] + pr[x][n][3];
+                }
+#pragma unroll
+            for (int x = 0; x < BL; ++x) {
+                uint32_t v0w[G], v1w[G];
+                lds_words<G>(v0w, blk + x * C::BB + 8 * D + lane * G * 4);
+                lds_words<G>(v1w, blk + x * C::BB + 8 * D + (32 + lane) * G * 4);
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
                     const uint32_t y0 = v0w[g] >> 8, y1 = v1w[g] >> 8;
                     const uint32_t a00 = v0w[g] & 0x000f000fu, a01 = v0w[g] & 0x00f000f0u;
                     const uint32_t a02 = v1w[g] & 0x000f000fu, a03 = v1w[g] & 0x00f000f0u;
                     const uint32_t a10 = y0 & 0x000f000fu, a11 = y0 & 0x00f000f0u;
                     const uint32_t a12 = y1 & 0x000f000fu, a13 = y1 & 0x00f000f0u;
+                    const float f0 = vs[x][0][g], f1 = vs[x][1][g], u0 = vl[x][0][g], u1 = vl[x][1][g];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float w0 = pr[n][0] * f0, w1 = pr[n][1] * f0, w2 = pr[n][2] * f1, w3 = pr[n][3] * f1;
-                        float u0 = pr[n][0] * vl[0][g], u1 = pr[n][1] * vl[0][g];
-                        float u2 = pr[n][2] * vl[1][g], u3 = pr[n][3] * vl[1][g];
-                        if (edge) {     // 0 times a NaN or an infinity that the row does not see
-                            if (hidden[n] & 1u) w0 = u0 = 0.f;
-                            if (hidden[n] & 2u) w1 = u1 = 0.f;
-                            if (hidden[n] & 4u) w2 = u2 = 0.f;
-                            if (hidden[n] & 8u) w3 = u3 = 0.f;
+                        const float(&P)[4] = pr[x][n];
+                        const float(&F)[4] = pf[x][n];
+                        float w0 = F[0] * f0, w1 = F[1] * f0, w2 = F[2] * f1, w3 = F[3] * f1;
+                        float(&o)[2] = ol[n][g];
+                        if constexpr (EDGE) {       // 0 times a NaN or an infinity that the row does not see
+                            const uint32_t no = hidden[x][n];
+                            if (no & 1u) w0 = 0.f; else o[0] = fmaf(P[0], u0, o[0]);
+                            if (no & 2u) w1 = 0.f; else o[1] = fmaf(P[1], u0, o[1]);
+                            if (no & 4u) w2 = 0.f; else o[0] = fmaf(P[2], u1, o[0]);
+                            if (no & 8u) w3 = 0.f; else o[1] = fmaf(P[3], u1, o[1]);
+                        } else {
+                            o[0] = fmaf(P[2], u1, fmaf(P[0], u0, o[0]));
+                            o[1] = fmaf(P[3], u1, fmaf(P[1], u0, o[1]));
                         }
-                        ol[n][g][0] += u0 + u2;
-                        ol[n][g][1] += u1 + u3;
                         const uint32_t b0 = movmatrix_trans(pack_f16x2(w0, w1));
                         const uint32_t b1 = movmatrix_trans(pack_f16x2(w2, w3));
-                        mma_f16(acc[n][2 * g], a00, a01, a02, a03, b0, b1);
-                        mma_f16(acc[n][2 * g + 1], a10, a11, a12, a13, b0, b1);
+                        mma_f16(acc[n][2 * g], a00, a01, a02, a03, b0, b1, acc[n][2 * g]);
+                        mma_f16(acc[n][2 * g + 1], a10, a11, a12, a13, b0, b1, acc[n][2 * g + 1]);
                     }
                 }
+            }
+        };
+        const int mine = att_steps<C::TILE, C::BL>(q, warp);
+        const int sb = q.seq.sb, wb0 = q.seq.wb0 - sb;
+        int li = q.t0 * C::TILE + warp * C::BL;
+        for (int i = 0; i < mine; ++i, li += C::TILE) {
+            ok = bounded_wait_warp(&full[cs], phase, abort, lim);
+            ++taken;
+            if (!ok) break;
+            const uint32_t on = valid >> (cs * C::BL) & ((1u << C::BL) - 1u);
+            if (on) {
+                int tb[C::BL];
+                bool inner = on == (1u << C::BL) - 1u;
+#pragma unroll
+                for (int x = 0; x < C::BL; ++x) {
+                    tb[x] = li + x < sb ? li + x : wb0 + li + x;
+                    inner = inner && tb[x] <= full_hi && (tb[x] >= full_lo || tb[x] < full_ns);
+                }
+                const uint8_t* blk = ring + cs * C::SB;
+                if (inner) step(blk, tb, on, std::false_type{});
+                else step(blk, tb, on, std::true_type{});
+            }
+            if (++cs == ST) {
+                cs = 0;
+                phase ^= 1u;
             }
             __syncwarp();           // every lane has read the stage
             fetch();
         }
-        // ---- this warp's part: O unnormalised in units of 2^m, m and l
-        float* orow = merge + warp * C::ROWS * C::OPAD;
-        float* ml = merge + kAttWarps * C::ROWS * C::OPAD + warp * C::ROWS * 2;
+        // ---- this warp's part: O unnormalised in units of 2^m, m and l (of rows 2c, 2c + 1)
+        float4 o[NT][2][G];         // channels 32·g + 4·gid ..
+        float m[NT][2];
         const float back = 1.f / fv;                       // exact: a power of two
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float lt = l[n][e];
+                m[n][e] = thr[n][e] == -INFINITY ? -INFINITY : -nm[n][e];
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-                const int r = n * 8 + 2 * c + e;
-                if (gid == 0) {
-                    ml[2 * r] = m[n][e];
-                    ml[2 * r + 1] = lt;
-                }
+                for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     float t = ol[n][g][e];
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                    for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
                     // channels 32·g + 4·gid + j; odd j were multiplied by 16
-                    *reinterpret_cast<float4*>(orow + r * C::OPAD + g * 32 + gid * 4) =
-                        make_float4(fmaf(acc[n][2 * g][e] * 0x1p24f, back, t),
-                                    fmaf(acc[n][2 * g][2 + e] * 0x1p20f, back, t),
-                                    fmaf(acc[n][2 * g + 1][e] * 0x1p24f, back, t),
-                                    fmaf(acc[n][2 * g + 1][2 + e] * 0x1p20f, back, t));
+                    o[n][e][g] = make_float4(fmaf(acc[n][2 * g][e] * 0x1p24f, back, t),
+                                             fmaf(acc[n][2 * g][2 + e] * 0x1p20f, back, t),
+                                             fmaf(acc[n][2 * g + 1][e] * 0x1p24f, back, t),
+                                             fmaf(acc[n][2 * g + 1][2 + e] * 0x1p20f, back, t));
                 }
             }
-        __syncthreads();
-        // ---- join the warps; whole segments are finished here, parts go to the workspace
-        const bool whole = t0 == 0 && t1 == nt_all;
-        float* part = a.ws + (2 * static_cast<size_t>(blockIdx.x) + (x == x0 ? 0 : 1)) * C::PART;
-        constexpr int C4 = D / 4;
-        for (int idx = threadIdx.x; idx < C::ROWS * C4; idx += kAttThreads) {
-            const int r = idx / C4, c4 = idx % C4;
-            if (row0 + r >= p.R) continue;
-            const float* mls = merge + kAttWarps * C::ROWS * C::OPAD + r * 2;
-            float M = -INFINITY, L = 0.f;
+        // ---- the warps' parts are joined in two rounds: 2 and 3 into 0 and 1, then 1 into 0
+        auto put = [&](float* slot) {
 #pragma unroll
-            for (int w = 0; w < kAttWarps; ++w) M = fmaxf(M, mls[w * C::ROWS * 2]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int w = 0; w < kAttWarps; ++w) {
-                const float mw = mls[w * C::ROWS * 2];
-                if (mw == -INFINITY) {
-                    L += mls[w * C::ROWS * 2 + 1];         // 0, or NaN when every score was
-                    continue;
+                for (int e = 0; e < 2; ++e) {
+                    const int r = n * 8 + 2 * c + e;
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        *reinterpret_cast<float4*>(slot + r * C::OPAD + g * 32 + gid * 4) = o[n][e][g];
+                    if (gid == 0)
+                        *reinterpret_cast<float2*>(slot + C::ROWS * C::OPAD + 2 * r) = make_float2(m[n][e], l[n][e]);
                 }
-                const float f = ex2_approx(mw - M);
-                L = fmaf(f, mls[w * C::ROWS * 2 + 1], L);
-                const float4 t = *reinterpret_cast<const float4*>(merge + (w * C::ROWS + r) * C::OPAD + c4 * 4);
-                o.x = fmaf(f, t.x, o.x); o.y = fmaf(f, t.y, o.y);
-                o.z = fmaf(f, t.z, o.z); o.w = fmaf(f, t.w, o.w);
-            }
-            if (whole) {
-                const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);    // NaN stays
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + (qbase + row0 + r) * D + c4 * 4;
-                *reinterpret_cast<uint2*>(dst) =
-                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-                if (c4 == 0) a.lse[qbase + row0 + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * kAttLn2;
-            } else {
-                *reinterpret_cast<float4*>(part + r * D + c4 * 4) = o;
-                if (c4 == 0) {
-                    part[C::ROWS * D + 2 * r] = M;
-                    part[C::ROWS * D + 2 * r + 1] = L;
+        };
+        auto take = [&](const float* slot) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = n * 8 + 2 * c + e;
+                    const float2 ml = *reinterpret_cast<const float2*>(slot + C::ROWS * C::OPAD + 2 * r);
+                    const float M = fmaxf(m[n][e], ml.x);
+                    // a part that saw no key has O = 0, and l = 0 or NaN when every score was
+                    const float fa = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - M);
+                    const float fb = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+                    l[n][e] = (m[n][e] == -INFINITY ? l[n][e] : fa * l[n][e]) + (ml.x == -INFINITY ? ml.y : fb * ml.y);
+                    m[n][e] = M;
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const float4 t = *reinterpret_cast<const float4*>(slot + r * C::OPAD + g * 32 + gid * 4);
+                        float4& w = o[n][e][g];
+                        w.x = fmaf(fb, t.x, fa * w.x); w.y = fmaf(fb, t.y, fa * w.y);
+                        w.z = fmaf(fb, t.z, fa * w.z); w.w = fmaf(fb, t.w, fa * w.w);
+                    }
                 }
-            }
-        }
+        };
+        const bool whole = q.t0 == 0 && q.t1 == att_tiles(q.seq, C::TILE);
+        float* part = a.ws + (2 * static_cast<size_t>(blockIdx.x) + (q.x == x0 ? 0 : 1)) * C::PART;
+        if (warp >= 2) put(merge + (warp - 2) * C::SLOT);
         __syncthreads();
-        // ---- next segment
-        x += t1 - t0;
-        tile = 0;
-        if (++hr == HR) {
-            hr = 0;
-            if (x < x1)
-                do seq = att_seq(a, ++b);
-                while (seq.nb == 0 && b + 1 < a.B);
-            if (seq.nb == 0) break;
+        if (threadIdx.x == kAttThreads - 1) sh->more = att_next<C::TILE>(a, sh->part, HR, x1);   // nobody reads it
+        if (warp < 2) take(merge + warp * C::SLOT);
+        if (warp == 1) put(merge + C::SLOT);
+        __syncthreads();
+        const bool more_parts = sh->more;
+        // ---- whole segments are finished here, parts go to the workspace
+        if (warp == 0) {
+            take(merge + C::SLOT);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = n * 8 + 2 * c + e;
+                    if (row0 + r >= p.R) continue;
+                    const float L = l[n][e];
+                    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);    // NaN stays
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const float4 w = o[n][e][g];
+                        if (whole)
+                            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + (qbase + row0 + r) * D +
+                                                      g * 32 + gid * 4) =
+                                make_uint2(pack_bf16x2(w.x * inv, w.y * inv), pack_bf16x2(w.z * inv, w.w * inv));
+                        else
+                            *reinterpret_cast<float4*>(part + r * D + g * 32 + gid * 4) = w;
+                    }
+                    if (gid == 0) {
+                        if (whole)
+                            a.lse[qbase + row0 + r] = L == 0.f ? -INFINITY : (m[n][e] + log2f(L)) * kAttLn2;
+                        else
+                            *reinterpret_cast<float2*>(part + C::ROWS * D + 2 * r) = make_float2(m[n][e], L);
+                    }
+                }
         }
+        if (!more_parts) break;
     }
     if (!ok || *abort) {          // let the copies in flight land
         const uint64_t t0 = globaltimer_ns();
@@ -820,58 +1032,110 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
 }
 
 // Joins the parts of segments that several runs share, and clears the rows of batch entries that see
-// no key. One CTA per (row, segment), a thread per channel.
+// no key. One CTA per (segment, row): teams of D / 4 lanes take every so many parts, so a long
+// sequence's parts (up to the number of runs) are read side by side.
+constexpr int kJoinThreads = 128;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(D) kv4_join_kernel(const AttParams p, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttParams p, int ctas) {
     using C = AttCfg<D, NT>;
-    __shared__ long long scratch[kAttWarps];
+    constexpr int LPP = D / 4, TEAMS = kJoinThreads / LPP;
+    __shared__ long long scratch[2][kJoinThreads / 32];
+    __shared__ float red[kJoinThreads / 32];
+    __shared__ float4 osum[TEAMS][LPP];
+    __shared__ float lsum[TEAMS];
     const Kv4AttendArgs& a = p.a;
     const int HR = a.pool.Hkv * p.RB;
     const int b = static_cast<int>(blockIdx.x / HR), hr = static_cast<int>(blockIdx.x % HR);
-    const int row = hr % p.RB * C::ROWS + static_cast<int>(blockIdx.y);
-    if (row >= p.R) return;
+    const int r = static_cast<int>(blockIdx.y), row = hr % p.RB * C::ROWS + r;
+    if (row >= p.R) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
+    const int team = threadIdx.x / LPP, lane4 = threadIdx.x % LPP;
     const size_t out = (static_cast<size_t>(b) * a.pool.Hkv + hr / p.RB) * p.R + row;
-    const int nt = att_tiles(a, b);
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + out * D + threadIdx.x;
+    uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + out * D) + lane4;
+    // tiles of the entries before b, of b, and of all
+    long long before = 0, total = 0;
+    for (int x = threadIdx.x; x < a.B; x += kJoinThreads) {
+        const int t = att_tiles(att_seq(a, x), C::TILE);
+        total += t;
+        if (x < b) before += t;
+    }
+    const int nt = att_tiles(att_seq(a, b), C::TILE);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, x);
+        before += __shfl_xor_sync(0xffffffffu, before, x);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        scratch[0][threadIdx.x >> 5] = total;
+        scratch[1][threadIdx.x >> 5] = before;
+    }
+    __syncthreads();
+    total = before = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+        total += scratch[0][w];
+        before += scratch[1][w];
+    }
+    total *= HR;
+    const long long runs = att_runs(total, ctas);
+    const long long xs = before * HR + static_cast<long long>(hr) * nt;
+    int r0 = 0, r1 = 0, slot0 = 0;
+    if (nt > 0) {
+        r0 = att_run_of(xs, total, runs);
+        r1 = att_run_of(xs + nt - 1, total, runs);
+        // the segment is the first of every run's but perhaps the first run's
+        slot0 = att_run_start(total, r0, runs) == xs ? 0 : 1;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // the runs' parts are there
     if (nt == 0) {
-        *o = __float2bfloat16_rn(0.f);
+        if (team == 0) *o = make_uint2(0u, 0u);
         if (threadIdx.x == 0) a.lse[out] = -INFINITY;
         return;
     }
-    const long long before = att_prefix(a, b, D, scratch);
-    const long long total = att_prefix(a, a.B, D, scratch) * HR;
-    const long long runs = att_runs(total, ctas);
-    const long long xs = before * HR + static_cast<long long>(hr) * nt, xe = xs + nt;
-    // run of tile x: the last r with total·r / runs <= x
-    const auto run_of = [&](long long x) {
-        long long r = x * runs / total;
-        while (r + 1 < runs && total * (r + 1) / runs <= x) ++r;
-        return r;
-    };
-    const long long r0 = run_of(xs), r1 = run_of(xe - 1);
     if (r0 == r1) return;                                  // one run held the whole segment
-    const int r = static_cast<int>(blockIdx.y);
-    const auto part_of = [&](long long run) {
-        const bool first = run > r0 || total * run / runs == xs;
-        return a.ws + (2 * static_cast<size_t>(run) + (first ? 0 : 1)) * C::PART;
+    const auto part_of = [&](int k) {
+        return a.ws + (2 * static_cast<size_t>(k) + (k == r0 ? slot0 : 0)) * C::PART;
     };
     float M = -INFINITY;
-    for (long long q = r0; q <= r1; ++q) M = fmaxf(M, part_of(q)[C::ROWS * D + 2 * r]);
-    float L = 0.f, v = 0.f;
-    for (long long q = r0; q <= r1; ++q) {
-        const float* part = part_of(q);
-        const float mq = part[C::ROWS * D + 2 * r];
-        if (mq == -INFINITY) {
-            L += part[C::ROWS * D + 2 * r + 1];
-            continue;
-        }
-        const float f = ex2_approx(mq - M);
-        L = fmaf(f, part[C::ROWS * D + 2 * r + 1], L);
-        v = fmaf(f, part[r * D + threadIdx.x], v);
+    for (int k = r0 + static_cast<int>(threadIdx.x); k <= r1; k += kJoinThreads)
+        M = fmaxf(M, part_of(k)[C::ROWS * D + 2 * r]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[w]);
+    float L = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = r0 + team; k <= r1; k += TEAMS) {
+        const float* part = part_of(k);
+        const float2 ml = *reinterpret_cast<const float2*>(part + C::ROWS * D + 2 * r);
+        const float4 t = *reinterpret_cast<const float4*>(part + r * D + lane4 * 4);
+        // a part that saw no key has O = 0, and l = 0 or NaN when every score was
+        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+        L += ml.x == -INFINITY ? ml.y : f * ml.y;
+        v.x = fmaf(f, t.x, v.x); v.y = fmaf(f, t.y, v.y);
+        v.z = fmaf(f, t.z, v.z); v.w = fmaf(f, t.w, v.w);
+    }
+    osum[team][lane4] = v;
+    if (lane4 == 0) lsum[team] = L;
+    __syncthreads();
+    if (team != 0) return;
+    L = 0.f;
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < TEAMS; ++w) {
+        L += lsum[w];
+        const float4 t = osum[w][lane4];
+        v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
     }
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    *o = __float2bfloat16_rn(v * inv);
-    if (threadIdx.x == 0) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * kAttLn2;
+    *o = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+    if (lane4 == 0) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * kAttLn2;
 }
 
 template <int D, int NT>
@@ -892,8 +1156,17 @@ cudaError_t launch_attend(const Kv4AttendArgs& a, cudaStream_t stream) {
     kv4_attend_kernel<D, NT><<<ctas, kAttThreads, C::SMEM, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rows = p.R < C::ROWS ? p.R : C::ROWS;
-    kv4_join_kernel<D, NT><<<dim3(static_cast<unsigned>(segs), rows), D, 0, stream>>>(p, ctas);
-    return cudaGetLastError();
+    // launched while the runs are still going, up to its wait for them
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(segs), static_cast<unsigned>(rows));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, p, ctas);
 }
 
 template <int D>

@@ -177,5 +177,5 @@ def attend(q, pool, table, lens, seqs, page_size, wl, wr, ns):
         el[b] = 2.0 ** -20 * size + 4e-6
         spread = np.abs(ve) + np.abs(ve).max(-1, keepdims=True)       # s q <= |value| + |lo|
         eo[b] = (BF16 * np.abs(o[b]) + (p @ spread)[0] * (2.0 ** -11 + 2 * el[b][..., None]) +
-                 2.0 ** -27 * vis.sum(1)[None, :, None] * np.abs(ve).max() * p.max(-1)[0][..., None]) * 1.02 + 1e-30
+                 2.0 ** -27 * vis.sum(1)[None, :, None] * np.abs(ve).max() * p.max(-1)[0][..., None]) * 1.02 + 1e-38
     return o, lse, eo, el
