@@ -29,67 +29,106 @@ __device__ __forceinline__ uint8_t* kv4_block(const Kv4Pool& p, int pg, int h, l
 }
 
 // ------------------------------------------------------------------------------------------
-// Append and gather. One CTA of 128 threads per (block of 16 tokens, head, batch entry); a team of 8
-// lanes holds a group of one token, 4 channels per lane, so minimum and maximum take three
-// shuffles, a lane's nibbles of V are one 16-bit unit and those of K half a word. Blocks that the
-// rows fill are put together in shared memory and copied out in 16-byte pieces; at the ragged
+// Append and gather. One CTA of 128 threads per (block of 16 tokens, head, batch entry); a team of 4
+// lanes holds a group of one token, 8 channels per lane: extrema take two shuffles, a lane's nibbles
+// of K are one word and those of V two 16-bit units, so nothing is exchanged to pack them. Blocks
+// that the rows fill are put together in shared memory and copied out in 16-byte pieces; at the ragged
 // ends each token's own 2- and 4-byte units are stored (neighbours' tokens are never touched).
-// Bound by HBM for long chunks, by latency (table entry, then store) for single tokens.
+// Bound by instruction issue for long chunks (about 12 per value), by latency (length, table entry,
+// then store) for single tokens.
 // ------------------------------------------------------------------------------------------
 constexpr int kRowThreads = 128;
 
-// q of x in a group with lo, s, from t = x - lo: the whole number nearest (x - lo)/s, ties to even.
-// t·(1/s) is within a few 2^-22 of the quotient, so it decides unless it lies next to a border; there
-// the exact border (n + 1/2)·s (s has 8 bits) is compared with t and what t lost of x - lo.
-__device__ __forceinline__ int kv4_quantise(float x, float lo, float s, float inv) {
-    const float t = x - lo;
-    const float f = t * inv;
-    float n = rintf(f);
-    if (fabsf(fabsf(f - n) - 0.5f) < 1e-4f) {
-        n = floorf(f);
-        const float border = (n + 0.5f) * s;              // exact: at most 5 + 8 bits
-        const float bb = t - x, lost = (x - (t - bb)) + (-lo - bb);   // x - lo = t + lost exactly
-        const bool up = t > border || (t == border && (lost > 0.f || (lost == 0.f && (static_cast<int>(n) & 1))));
-        n = up ? n + 1.f : n;
-    }
-    return static_cast<int>(fminf(fmaxf(n, 0.f), 15.f));
+__device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {       // NaN if either is
+    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// One lane's 4 channels (bf16 in w) of a group shared by 8 lanes: nibbles (channel i in bits 4·i) and
-// the group's parameter word.
-__device__ __forceinline__ uint32_t kv4_group(uint2 w, uint32_t& param) {
-    float x[4];
-    x[0] = __uint_as_float(w.x << 16);
-    x[1] = __uint_as_float(w.x & 0xffff0000u);
-    x[2] = __uint_as_float(w.y << 16);
-    x[3] = __uint_as_float(w.y & 0xffff0000u);
-    float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
-    float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    bool nan = !(x[0] == x[0] && x[1] == x[1] && x[2] == x[2] && x[3] == x[3]);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        nan |= __shfl_xor_sync(0xffffffffu, nan, o);
+// One lane's 8 channels (bf16 in w) of a group shared by 4 lanes: whole numbers, each in the low bits
+// of a word, and the group's parameter word. Least and greatest travel as one word (lo, -hi), both by
+// minima. (x - lo)/s is taken as t·(1/s), t = x - lo, within a few 2^-22 of it, which decides unless it
+// lies next to a border; there what is left of t, t - n·s (exact: n·s has 12 bits), is compared with
+// s/2. Exact ties are common among bf16 values (1 in 500, 40% of the warps), so that path is short.
+// Likewise s = (hi - lo)/15 before its rounding to bf16. No quotient exceeds 15.1: s is at least
+// (1 - 2^-8) of a 15th of the range.
+__device__ __forceinline__ void kv4_group(uint4 w, uint32_t (&n)[8], uint32_t& param) {
+    constexpr uint32_t kNeg = 0x80008000u;
+    const uint32_t least = bmin2(bmin2(w.x, w.y), bmin2(w.z, w.w));
+    const uint32_t most = bmin2(bmin2(w.x ^ kNeg, w.y ^ kNeg), bmin2(w.z ^ kNeg, w.w ^ kNeg));
+    uint32_t e = bmin2(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
+    e = bmin2(e, __shfl_xor_sync(0xffffffffu, e, 1));
+    e = bmin2(e, __shfl_xor_sync(0xffffffffu, e, 2));
+    const float lo = __uint_as_float(e << 16), range = -__uint_as_float(e & 0xffff0000u) - lo;
+    float s = range * (1.f / 15.f);
+    if ((__float_as_uint(s) & 0xffffu) - 0x7ffeu <= 4u) s = __fdiv_rn(range, 15.f);
+    uint32_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+    s = __uint_as_float(sb << 16);
+    float inv = __fdividef(1.f, s);                       // s < 2^125
+    if (!(s >= 0x1p-100f && s < INFINITY)) {
+        // nothing to tell apart, or a NaN or an infinity, which make the whole group NaN
+        sb = s < 0x1p-100f ? 0u : 0x7fc0u;
+        s = inv = 0.f;
     }
-    uint32_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(hi - lo, 15.f)));
-    float s = __uint_as_float(sb << 16);
-    if (s < 0x1p-100f) { s = 0.f; sb = 0; }
-    // a NaN or an infinity makes its whole group NaN
-    if (nan || !(s < INFINITY)) { sb = 0x7fc0u; s = 0.f; }
-    param = sb | (__float_as_uint(lo) & 0xffff0000u);
-    if (s == 0.f) return 0;
-    const float inv = 1.f / s;
-    uint32_t n = 0;
+    param = sb | e << 16;
+    constexpr float kWhole = 12582912.f;                  // 1.5·2^23: adding it rounds to a whole number
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    float far = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n |= static_cast<uint32_t>(kv4_quantise(x[i], lo, s, inv)) << (4 * i);
-    return n;
+    for (int i = 0; i < 8; ++i) {
+        const float t = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16) - lo;
+        const float r = fmaf(t, inv, kWhole);
+        far = fmaxf(far, fabsf(fmaf(t, inv, kWhole - r)));
+        n[i] = __float_as_uint(r);
+    }
+    if (far > 0.4999f) {
+        const float half = 0.5f * s;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16), t = x - lo;
+            const float rest = fmaf(kWhole - __uint_as_float(n[i]), s, t);
+            if (fabsf(rest) >= half) {
+                // t may have lost some of x - lo; at a tie that decides, or else the even number
+                const float b = t - x, lost = copysignf(1.f, rest) * ((x - (t - b)) + (-lo - b));
+                const bool out = fabsf(rest) > half || lost > 0.f || (lost == 0.f && (n[i] & 1u));
+                if (out) n[i] += rest > 0.f ? 1u : 0xffffffffu;
+            }
+        }
+    }
+    if (s == 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = 0;
+    }
+}
+
+// A team's task of round x: K or V, token of the block, group. kRowThreads / 4 = 32 teams take the
+// 2·16·G tasks in G rounds; a warp's tasks of one round are all K or all V.
+struct RowTask {
+    int kv, tok, g;
+};
+template <int G>
+__device__ __forceinline__ RowTask row_task(int x) {
+    const int id = x * (kRowThreads / 4) + (threadIdx.x >> 2);
+    return RowTask{id / (16 * G), id % (16 * G) / G, id % G};
+}
+
+// Bytes of a token's group in its block: K word of lane c, first V unit of lane c (the second lies 16·G
+// bytes on: the next row), parameters.
+template <int D>
+__device__ __forceinline__ int kv4_k_at(int tok, int g, int c) {
+    return (((tok >> 3) * 32 + (tok & 7) * 4 + c) * (D / 32) + g) * 4;
+}
+template <int D>
+__device__ __forceinline__ int kv4_v_at(int tok, int g, int c) {
+    return 8 * D + (((tok >> 3) * 32 + 8 * c + ((tok & 7) >> 1)) * (D / 32) + g) * 4 + (tok & 1) * 2;
+}
+template <int D>
+__device__ __forceinline__ int kv4_p_at(int kv, int tok, int g) {
+    return (16 + 2 * kv) * D + (tok * (D / 32) + g) * 4;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowsArgs a) {
     constexpr int G = D / 32, BB = kv4_block_bytes(D);
-    constexpr int TASKS = 16 * G;                        // (token, group), by teams of 8 lanes
     __shared__ __align__(16) uint8_t stage[BB];
     const int i = blockIdx.z, h = blockIdx.y;
     const int first = a.start[i];
@@ -98,49 +137,43 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowsAr
     const long long blk = first / kKv4Block + static_cast<long long>(blockIdx.x);
     const long long t0 = blk * kKv4Block - first;        // row of the block's first token
     if (t0 >= count) return;
+    const bool whole = t0 >= 0 && t0 + kKv4Block <= count;
+    const int lo = t0 < 0 ? static_cast<int>(-t0) : 0;   // tokens [lo, hi) of the block are rows
+    const int hi = static_cast<int>(min(count - t0, static_cast<long long>(kKv4Block)));
     const int slot = a.pool.seqs ? a.pool.seqs[i] : i;
+    const int c = threadIdx.x & 3;
+    const long long base = (static_cast<long long>(i) * a.pool.Hkv + h) * a.n + t0;
+    uint4 w[G];
+#pragma unroll
+    for (int x = 0; x < G; ++x) {        // all loads before the first use, and before the page's number
+        const RowTask t = row_task<G>(x);
+        w[x] = make_uint4(0u, 0u, 0u, 0u);
+        if (t.tok >= lo && t.tok < hi)
+            w[x] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(t.kv ? a.v : a.k) +
+                                                   (base + t.tok) * D + t.g * 32 + c * 8);
+    }
     const int pg = kv4_page(a.pool, slot, blk * kKv4Block);
     if (pg < 0) return;
     uint8_t* block = kv4_block(a.pool, pg, h, blk * kKv4Block);
-    const bool whole = t0 >= 0 && t0 + kKv4Block <= count;
     uint8_t* out = whole ? stage : block;
-    const int team = threadIdx.x >> 3, row = threadIdx.x & 7;
-    const size_t base = (static_cast<size_t>(i) * a.pool.Hkv + h) * a.n * D;
-    const __nv_bfloat16* src[2] = {static_cast<const __nv_bfloat16*>(a.k) + base,
-                                   static_cast<const __nv_bfloat16*>(a.v) + base};
-    uint2 w[2][G];
-#pragma unroll
-    for (int x = 0; x < G; ++x) {                        // all loads before the first use
-        const int task = x * (kRowThreads / 8) + team;
-        const long long t = t0 + task / G;
-        const bool live = t >= 0 && t < count;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-            w[kv][x] = live ? *reinterpret_cast<const uint2*>(src[kv] + t * D + task % G * 32 + row * 4)
-                            : make_uint2(0u, 0u);
-    }
-    static_assert(TASKS == G * (kRowThreads / 8), "one task per team and round");
 #pragma unroll
     for (int x = 0; x < G; ++x) {
-        const int task = x * (kRowThreads / 8) + team;
-        const int tok = task / G, g = task % G;
-        const bool live = t0 + tok >= 0 && t0 + tok < count;
-        uint32_t kp, vp;
-        uint32_t kn = kv4_group(w[0][x], kp), vn = kv4_group(w[1][x], vp);
-        // K: channels 4·row .. 4·row+3 are j = 2·(row & 1) + {0, 0, 1, 1}, h = {0, 1, 0, 1} of word
-        // c = row / 2: nibbles to bits 4·(j + 4·h)
-        kn = (kn & 0xfu) | (kn & 0xf0u) << 12 | (kn & 0xf00u) >> 4 | (kn & 0xf000u) << 8;
-        kn <<= 8 * (row & 1);
-        kn |= __shfl_xor_sync(0xffffffffu, kn, 1);
-        if (!live) continue;
-        if (!(row & 1)) {
-            const int word = ((tok >> 3) * 32 + (tok & 7) * 4 + (row >> 1)) * G + g;
-            *reinterpret_cast<uint32_t*>(out + word * 4) = kn;
+        const RowTask t = row_task<G>(x);
+        uint32_t n[8], param;
+        kv4_group(w[x], n, param);
+        if (t.tok < lo || t.tok >= hi) continue;
+        if (t.kv == 0) {
+            const uint32_t even = n[0] + (n[2] << 4) + (n[4] << 8) + (n[6] << 12);
+            const uint32_t odd = n[1] + (n[3] << 4) + (n[5] << 8) + (n[7] << 12);
+            *reinterpret_cast<uint32_t*>(out + kv4_k_at<D>(t.tok, t.g, c)) = __byte_perm(even, odd, 0x5410);
+        } else {
+            uint8_t* v = out + kv4_v_at<D>(t.tok, t.g, c);
+            *reinterpret_cast<uint16_t*>(v) =
+                static_cast<uint16_t>(n[0] + (n[1] << 4) + (n[2] << 8) + (n[3] << 12));
+            *reinterpret_cast<uint16_t*>(v + 16 * G) =
+                static_cast<uint16_t>(n[4] + (n[5] << 4) + (n[6] << 8) + (n[7] << 12));
         }
-        const int unit = (((tok >> 3) * 32 + row * 4 + ((tok & 7) >> 1)) * G + g) * 2 + (tok & 1);
-        *reinterpret_cast<uint16_t*>(out + 8 * D + unit * 2) = static_cast<uint16_t>(vn);
-        if (row < 2)
-            *reinterpret_cast<uint32_t*>(out + 16 * D + row * 2 * D + (tok * G + g) * 4) = row ? vp : kp;
+        if (c == 0) *reinterpret_cast<uint32_t*>(out + kv4_p_at<D>(t.kv, t.tok, t.g)) = param;
     }
     if (whole) {
         __syncthreads();
@@ -169,36 +202,42 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4RowsAr
             reinterpret_cast<uint4*>(stage)[x] = reinterpret_cast<const uint4*>(block)[x];
     }
     __syncthreads();
-    const int team = threadIdx.x >> 3, row = threadIdx.x & 7;
-    const size_t base = (static_cast<size_t>(i) * a.pool.Hkv + h) * a.n * D;
+    const int c = threadIdx.x & 3;
+    const int lo = t0 < 0 ? static_cast<int>(-t0) : 0;   // tokens [lo, hi) are rows, [lo, held) in use
+    const int hi = static_cast<int>(min(a.n - t0, static_cast<long long>(kKv4Block)));
+    const int held = pg < 0 ? 0 : static_cast<int>(min(count - t0, static_cast<long long>(kKv4Block)));
+    const long long base = (static_cast<long long>(i) * a.pool.Hkv + h) * a.n + t0;
 #pragma unroll
     for (int x = 0; x < G; ++x) {
-        const int task = x * (kRowThreads / 8) + team;
-        const int tok = task / G, g = task % G;
-        const long long t = t0 + tok;
-        if (t < 0 || t >= a.n) continue;
-        uint2 w[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
-        if (pg >= 0 && t < count) {
-            const uint32_t kw = *reinterpret_cast<const uint32_t*>(
-                stage + (((tok >> 3) * 32 + (tok & 7) * 4 + (row >> 1)) * G + g) * 4) >> (8 * (row & 1));
-            const uint32_t vw = *reinterpret_cast<const uint16_t*>(
-                stage + 8 * D + ((((tok >> 3) * 32 + row * 4 + ((tok & 7) >> 1)) * G + g) * 2 + (tok & 1)) * 2);
-            const uint32_t nib[2] = {(kw & 0xfu) | (kw >> 12 & 0xf0u) | (kw << 4 & 0xf00u) | (kw >> 8 & 0xf000u),
-                                     vw};
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const uint32_t p = *reinterpret_cast<const uint32_t*>(stage + (16 + 2 * kv) * D + (tok * G + g) * 4);
-                const float s = __uint_as_float(p << 16), lo = __uint_as_float(p & 0xffff0000u);
-                float y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    y[e] = fmaf(s, static_cast<float>(nib[kv] >> (4 * e) & 15u), lo);
-                w[kv] = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+        const RowTask t = row_task<G>(x);
+        if (t.tok < lo || t.tok >= hi) continue;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (t.tok < held) {
+            uint32_t n[2];               // 4 nibbles each: channels 0 .. 3 and 4 .. 7
+            if (t.kv == 0) {             // channels (0, 1), (2, 3) .. in bits 4·j and 4·j + 16
+                const uint32_t k = *reinterpret_cast<const uint32_t*>(stage + kv4_k_at<D>(t.tok, t.g, c));
+                n[0] = (k & 0xfu) | (k >> 12 & 0xf0u) | (k << 4 & 0xf00u) | (k >> 8 & 0xf000u);
+                const uint32_t k2 = k >> 8;
+                n[1] = (k2 & 0xfu) | (k2 >> 12 & 0xf0u) | (k2 << 4 & 0xf00u) | (k2 >> 8 & 0xf000u);
+            } else {
+                const uint8_t* v = stage + kv4_v_at<D>(t.tok, t.g, c);
+                n[0] = *reinterpret_cast<const uint16_t*>(v);
+                n[1] = *reinterpret_cast<const uint16_t*>(v + 16 * G);
             }
+            const uint32_t p = *reinterpret_cast<const uint32_t*>(stage + kv4_p_at<D>(t.kv, t.tok, t.g));
+            const float s = __uint_as_float(p << 16), least = __uint_as_float(p & 0xffff0000u);
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // 2^23 + q, less 2^23: cheaper than a conversion
+                const float q0 = __uint_as_float((n[e / 2] >> (8 * (e % 2)) & 15u) | 0x4b000000u) - 8388608.f;
+                const float q1 = __uint_as_float((n[e / 2] >> (8 * (e % 2) + 4) & 15u) | 0x4b000000u) - 8388608.f;
+                y[e] = pack_bf16x2(fmaf(s, q0, least), fmaf(s, q1, least));
+            }
+            w = make_uint4(y[0], y[1], y[2], y[3]);
         }
-        const size_t at = base + t * D + g * 32 + row * 4;
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.k) + at) = w[0];
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.v) + at) = w[1];
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(t.kv ? a.v : a.k) + (base + t.tok) * D + t.g * 32 +
+                                  c * 8) = w;
     }
 }
 
@@ -238,10 +277,13 @@ struct AttCfg {
     static constexpr int G = D / 32;
     static constexpr int BB = kv4_block_bytes(D);
     static constexpr int ROWS = 8 * NT;
-    static constexpr int BL = NT == 1 ? 2 : 1;                          // blocks a warp takes per step
+    // blocks a warp takes per step: two where they hide each other's latency and registers allow (d =
+    // 128: 50 against 58 us on one sequence of 131072); with smaller d one (16 sequences, 4 rows, d 64,
+    // window 1024: 17.2 against 18.6 us)
+    static constexpr int BL = NT == 1 && D == 128 ? 2 : 1;
     static constexpr int TILE = kAttWarps * BL;                         // blocks per tile
     static constexpr int SB = BL * BB;                                  // bytes per stage
-    static constexpr int STAGES = NT == 1 ? (D == 128 ? 3 : (D == 64 ? 4 : 6)) : (D == 128 ? 4 : 8);
+    static constexpr int STAGES = D == 128 ? (NT == 1 ? 3 : 4) : 8;
     static constexpr int CTAS = NT == 1 ? (D == 128 ? 3 : 4) : 2;       // per SM
     static constexpr int RING = kAttWarps * STAGES * SB;
     static constexpr int OPAD = D + 4;
@@ -315,8 +357,23 @@ __device__ __forceinline__ long long att_scan(long long v, long long* all, long 
     return before + incl - v;
 }
 
-// Runs that `total` tiles are cut into (one per CTA), and the first tile of run k. Almost always
-// 32 bits do: a 64-bit division takes ten times as long, and every CTA waits for it.
+// The line that is cut into runs: segment after segment, each kAttSwitch places for beginning it (a
+// CTA that holds many short segments would finish last otherwise: 64 sequences of 1 to 8192 tokens
+// took 112 us without, 103, 89, 87 and 89 us with 1, 3, 4 and 6 places) and one place per tile. Where runs are short anyway, the
+// switches are not counted. (tiles, segments) of the entries below one are summed in one word.
+constexpr int kAttSwitch = 4;
+__device__ __forceinline__ long long att_pair(const AttSeq& s, int tile) {
+    return s.nb > 0 ? static_cast<long long>(att_tiles(s, tile)) << 16 | 1 : 0;
+}
+__device__ __forceinline__ int att_switch(long long pairs, int HR, int ctas) {
+    return (pairs >> 16) * HR >= 4LL * ctas ? kAttSwitch : 0;
+}
+__device__ __forceinline__ long long att_line(long long pairs, int HR, int sw) {
+    return ((pairs >> 16) + (pairs & 0xffff) * sw) * HR;
+}
+
+// Runs that a line of `total` places is cut into (one per CTA), and the first place of run k. Almost
+// always 32 bits do: a 64-bit division takes ten times as long, and every CTA waits for it.
 __host__ __device__ inline long long att_runs(long long total, int ctas) {
     return total < ctas ? total : ctas;
 }
@@ -324,7 +381,7 @@ __device__ __forceinline__ long long att_run_start(long long total, int k, long 
     if (total < (1LL << 22)) return static_cast<unsigned>(total) * static_cast<unsigned>(k) / static_cast<unsigned>(runs);
     return total * k / runs;
 }
-// Run that holds tile x: the last k with total·k / runs <= x.
+// Run that holds place x: the last k with total·k / runs <= x.
 __device__ __forceinline__ int att_run_of(long long x, long long total, long long runs) {
     long long k = total < (1LL << 22) ? static_cast<unsigned>(x) * static_cast<unsigned>(runs) / static_cast<unsigned>(total)
                                       : x * runs / total;
@@ -386,12 +443,13 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[G], const uint8_t* p) {
     }
 }
 
-// A run's place: batch entry, (K/V head, row block), the tiles [t0, t1) of that segment that the run
-// holds, and the run's tiles before them.
+// A run's part of a segment: batch entry, (K/V head, row block), the tiles [t0, t1) that the run holds,
+// the place of t0 on the line, and which of the run's parts it is.
 struct AttPart {
     AttSeq seq;
     int b, hr, t0, t1;
     long long x;
+    int number;
 };
 
 struct AttShared {
@@ -407,10 +465,12 @@ __device__ __forceinline__ void att_clip(AttPart& q, long long x1) {
     q.t1 = static_cast<int>(min(static_cast<long long>(att_tiles(q.seq, TILE)), q.t0 + (x1 - q.x)));
 }
 template <int TILE>
-__device__ __forceinline__ bool att_next(const Kv4AttendArgs& a, AttPart& q, int HR, long long x1) {
-    q.x += q.t1 - q.t0;
+__device__ __forceinline__ bool att_next(const Kv4AttendArgs& a, AttPart& q, int HR, int sw, long long x1) {
+    if (q.t1 < att_tiles(q.seq, TILE)) return false;
+    q.x += q.t1 - q.t0 + sw;
     if (q.x >= x1) return false;
     q.t0 = 0;
+    ++q.number;
     if (++q.hr == HR) {
         q.hr = 0;
         do {
@@ -454,7 +514,8 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");    // the joining launch may be set up
     // ---- this CTA's run of tiles, and the segment it begins in
     const int HR = a.pool.Hkv * p.RB;
-    long long x0, x1;
+    long long x1;
+    int sw;
     {
         // a thread per batch entry; the one that holds the run's first tile writes down the place.
         // More entries than threads: chunks of them, once for the total and once for the place
@@ -465,13 +526,14 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
             mine.nb = 0;
             if (b < a.B) mine = att_seq(a, b);
             long long all;
-            before = total + att_scan(att_tiles(mine, C::TILE), &all, sh->scratch);
+            before = total + att_scan(att_pair(mine, C::TILE), &all, sh->scratch);
             total += all;
         }
-        total *= HR;
+        sw = att_switch(total, HR, gridDim.x);
+        total = att_line(total, HR, sw);
         const long long runs = att_runs(total, gridDim.x);
         if (blockIdx.x >= runs) return;
-        x0 = att_run_start(total, blockIdx.x, runs);
+        const long long x0 = att_run_start(total, blockIdx.x, runs);
         x1 = att_run_start(total, blockIdx.x + 1, runs);
         long long chunk = 0;
         for (int b0 = 0; b0 < a.B; b0 += kAttThreads) {
@@ -480,26 +542,28 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
                 mine.nb = 0;
                 if (b < a.B) mine = att_seq(a, b);
                 long long all;
-                before = chunk + att_scan(att_tiles(mine, C::TILE), &all, sh->scratch);
+                before = chunk + att_scan(att_pair(mine, C::TILE), &all, sh->scratch);
                 chunk += all;
             }
             const int nt = att_tiles(mine, C::TILE);
-            if (nt > 0 && x0 >= before * HR && x0 < (before + nt) * HR) {
+            const long long at = x0 - att_line(before, HR, sw), each = nt + sw;
+            if (nt > 0 && at >= 0 && at < each * HR) {
                 AttPart q;
-                const long long tile = x0 - before * HR;
                 q.seq = mine;
                 q.b = b;
-                q.x = x0;
-                q.hr = static_cast<int>(tile < (1LL << 31) ? static_cast<unsigned>(tile) / static_cast<unsigned>(nt)
-                                                           : tile / nt);
-                q.t0 = static_cast<int>(tile - static_cast<long long>(q.hr) * nt);
+                q.number = 0;
+                q.hr = static_cast<int>(at < (1LL << 31) ? static_cast<unsigned>(at) / static_cast<unsigned>(each)
+                                                         : at / each);
+                q.t0 = max(static_cast<int>(at - q.hr * each) - sw, 0);
+                q.x = x0 - at + q.hr * each + sw + q.t0;
+                if (q.x >= x1) continue;               // the run has places but no tile
                 att_clip<C::TILE>(q, x1);
                 sh->part = q;
                 for (int w = 0; w < kAttWarps; ++w) sh->fetch[w] = q;
             }
         }
         __syncthreads();
-        if (sh->part.b < 0) return;        // only if lens changed under the call
+        if (sh->part.b < 0) return;        // no tile
     }
     const AttPart& q = sh->part;
     const int bpp = a.pool.page_size / kKv4Block;
@@ -533,7 +597,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
         while (left == 0) {
             __syncwarp();
             int go = 0;
-            if (lane == 0) go = att_next<C::TILE>(a, f, HR, x1);
+            if (lane == 0) go = att_next<C::TILE>(a, f, HR, sw, x1);
             go = __shfl_sync(0xffffffffu, go, 0);
             __syncwarp();
             if (!go) {
@@ -984,10 +1048,10 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
                 }
         };
         const bool whole = q.t0 == 0 && q.t1 == att_tiles(q.seq, C::TILE);
-        float* part = a.ws + (2 * static_cast<size_t>(blockIdx.x) + (q.x == x0 ? 0 : 1)) * C::PART;
+        float* part = a.ws + (2 * static_cast<size_t>(blockIdx.x) + (q.number == 0 ? 0 : 1)) * C::PART;
         if (warp >= 2) put(merge + (warp - 2) * C::SLOT);
         __syncthreads();
-        if (threadIdx.x == kAttThreads - 1) sh->more = att_next<C::TILE>(a, sh->part, HR, x1);   // nobody reads it
+        if (threadIdx.x == kAttThreads - 1) sh->more = att_next<C::TILE>(a, sh->part, HR, sw, x1);   // nobody reads it
         if (warp < 2) take(merge + warp * C::SLOT);
         if (warp == 1) put(merge + C::SLOT);
         __syncthreads();
@@ -1055,10 +1119,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttParams 
     const int team = threadIdx.x / LPP, lane4 = threadIdx.x % LPP;
     const size_t out = (static_cast<size_t>(b) * a.pool.Hkv + hr / p.RB) * p.R + row;
     uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + out * D) + lane4;
-    // tiles of the entries before b, of b, and of all
+    // (tiles, segments) of the entries before b and of all
     long long before = 0, total = 0;
     for (int x = threadIdx.x; x < a.B; x += kJoinThreads) {
-        const int t = att_tiles(att_seq(a, x), C::TILE);
+        const long long t = att_pair(att_seq(a, x), C::TILE);
         total += t;
         if (x < b) before += t;
     }
@@ -1079,15 +1143,16 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttParams 
         total += scratch[0][w];
         before += scratch[1][w];
     }
-    total *= HR;
+    const int sw = att_switch(total, HR, ctas);
+    total = att_line(total, HR, sw);
     const long long runs = att_runs(total, ctas);
-    const long long xs = before * HR + static_cast<long long>(hr) * nt;
+    const long long seg = att_line(before, HR, sw) + static_cast<long long>(hr) * (nt + sw), xs = seg + sw;
     int r0 = 0, r1 = 0, slot0 = 0;
     if (nt > 0) {
         r0 = att_run_of(xs, total, runs);
         r1 = att_run_of(xs + nt - 1, total, runs);
         // the segment is the first of every run's but perhaps the first run's
-        slot0 = att_run_start(total, r0, runs) == xs ? 0 : 1;
+        slot0 = att_run_start(total, r0, runs) >= seg ? 0 : 1;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");     // the runs' parts are there
     if (nt == 0) {
