@@ -25,32 +25,34 @@ constexpr int kPgTile = 4 * kPgThreads;       // pages one CTA looks at per step
 constexpr int kPgCluster = 8;
 constexpr int kErrPages = 6;                  // ATTN_ERR_PAGES
 
-// Inclusive prefix sum over the CTA's threads; *total gets the sum. Synchronises the CTA.
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T* total, T* warp_sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-    }
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-        T s = warp_sums[lane];
+// Inclusive prefix sums over the CTA's threads, with one barrier each: every warp scans the warps' sums
+// for itself, and two buffers take turns, so that one is rewritten only a barrier after it was read.
+struct BlockScan {
+    long long* sums;      // 2 x kPgWarps
+    int turn = 0;
+    __device__ __forceinline__ long long operator()(long long v, long long* total) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const T y = __shfl_up_sync(0xffffffffu, s, o);
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        long long* buf = sums + turn * kPgWarps;
+        turn ^= 1;
+        if (lane == 31) buf[warp] = v;
+        __syncthreads();
+        long long s = buf[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += y;
         }
-        warp_sums[lane] = s;
+        *total = __shfl_sync(0xffffffffu, s, kPgWarps - 1);
+        const long long before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+        return warp > 0 ? v + before : v;
     }
-    __syncthreads();
-    if (warp > 0) v += warp_sums[warp - 1];
-    *total = warp_sums[kPgWarps - 1];
-    __syncthreads();
-    return v;
-}
+};
+static_assert(kPgWarps == 32, "one lane per warp's sum");
 
 // refs of pages p .. p+3 (p a multiple of 4); pages past the end read as in use.
 __device__ __forceinline__ int4 refs4(const int* refs, int p, int pages) {
@@ -86,11 +88,21 @@ __global__ void __launch_bounds__(kPgThreads) pages_take_kernel(const PageState 
     const int words = (s.slots + 31) / 32;
     int* pre = reinterpret_cast<int*>(marks + words);                    // pages needed before entry i
     int* len = pre + n + 1;                                              // tokens before the call
-    __shared__ long long sums[kPgWarps];
+    __shared__ long long sums[2 * kPgWarps];
     __shared__ int isums[kPgWarps];
     __shared__ int free_here;
+    BlockScan scan{sums};
     const int rank = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
     const int cap = s.max_pages * s.page_size;
+    // ---- free pages of this CTA's slice (their counts arrive while the entries are read)
+    int begin, end;
+    slice_of(s.pages, rank, ctas, begin, end);
+    int mine = 0;
+    int4 r4 = make_int4(1, 1, 1, 1);
+    for (int p = begin + 4 * tid; p < end; p += kPgTile) {
+        r4 = refs4(s.refs, p, s.pages);
+        mine += (r4.x == 0) + (r4.y == 0) + (r4.z == 0) + (r4.w == 0);
+    }
     // ---- the call's entries: in range, each row once, room in the table (every CTA for itself)
     for (int i = tid; i < words; i += kPgThreads) marks[i] = 0;
     __syncthreads();
@@ -130,23 +142,14 @@ __global__ void __launch_bounds__(kPgThreads) pages_take_kernel(const PageState 
             len[i] = have;
         }
         long long part;
-        const long long incl = block_scan(need, &part, sums);
+        const long long incl = scan(need, &part);
         if (i < n) pre[i] = static_cast<int>(min(need_all + incl - need, 0x7fffffffLL));
         need_all += part;
     }
     if (tid == 0) pre[n] = static_cast<int>(min(need_all, 0x7fffffffLL));
-    // ---- free pages of this CTA's slice
-    int begin, end;
-    slice_of(s.pages, rank, ctas, begin, end);
-    int mine = 0;
-    int4 r4 = make_int4(1, 1, 1, 1);
-    for (int p = begin + 4 * tid; p < end; p += kPgTile) {
-        r4 = refs4(s.refs, p, s.pages);
-        mine += (r4.x == 0) + (r4.y == 0) + (r4.z == 0) + (r4.w == 0);
-    }
-    int total;
-    block_scan(mine, &total, isums);
-    if (tid == 0) free_here = total;
+    long long total;
+    const long long mine_incl = scan(mine, &total);
+    if (tid == 0) free_here = static_cast<int>(total);
     bad = __syncthreads_or(bad);
     cluster.sync();                                    // all have read lens, all counts are there
     int before = 0, free_all = 0;
@@ -163,9 +166,10 @@ __global__ void __launch_bounds__(kPgThreads) pages_take_kernel(const PageState 
         if (end - begin > kPgTile) r4 = p < end ? refs4(s.refs, p, s.pages) : make_int4(1, 1, 1, 1);
         const int zero[4] = {r4.x == 0, r4.y == 0, r4.z == 0, r4.w == 0};
         const int here = zero[0] + zero[1] + zero[2] + zero[3];
-        int tile;
-        int r = before + block_scan(here, &tile, isums) - here;
-        before += tile;
+        long long tile = total, incl = mine_incl;          // a slice of one tile has been scanned
+        if (end - begin > kPgTile) incl = scan(here, &tile);
+        int r = before + static_cast<int>(incl) - here;
+        before += static_cast<int>(tile);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (!zero[e]) continue;
@@ -259,28 +263,52 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const PageState s, cons
     if (whole && threadIdx.x == 0) s.lens[q] = 0;
 }
 
+// Compaction, second part: the table's entries and the counts follow the pages (all threads of the
+// grid). A rank is read for entries that name a page in use, which is in the plan; others are left.
+__device__ __forceinline__ void pages_follow(int* table, long long entries, int* refs, int pages, const int* from,
+                                             const int* to, const int* rank_of, int low, int all) {
+    if (all == 0) return;
+    const long long t0 = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const long long nt = static_cast<long long>(gridDim.x) * blockDim.x;
+    for (long long r = t0; r < all; r += nt) {
+        const int a = from[r];
+        refs[to[r]] = refs[a];
+        refs[a] = 0;
+    }
+#pragma unroll 4
+    for (long long i = t0; i < entries; i += nt) {
+        const int p = table[i];
+        if (p < low || p >= pages) continue;
+        const int r = rank_of[p];
+        if (r >= 0 && r < all && from[r] == p) table[i] = to[r];
+    }
+}
+
 // Compaction, first part: with L pages in use, those numbered L and above (movers) go to the free
 // pages below L (holes), both in ascending order. from[r] -> to[r], rank[p] = r of mover p,
 // meta = {L, movers}.
-__global__ void __launch_bounds__(kPgThreads) pages_plan_kernel(const int* __restrict__ refs, int pages,
+__global__ void __launch_bounds__(kPgThreads) pages_plan_kernel(const int* refs, int pages,
                                                                 int* from, int* to, int* count, int* rank_of,
-                                                                int* meta, int cap, int ctas) {
+                                                                int* meta, int cap, int ctas, int* table,
+                                                                long long entries, int* refs_out) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
-    __shared__ int sums[kPgWarps];
+    __shared__ long long sums[2 * kPgWarps];
     __shared__ int here[3];                            // used pages, movers, holes of this slice
+    BlockScan scan{sums};
     const int rank = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
     int begin, end;
     slice_of(pages, rank, ctas, begin, end);
     const bool one = end - begin <= kPgTile;
     int4 r4 = make_int4(0, 0, 0, 0);
-    int used = 0, total;
+    int used = 0;
+    long long total;
     for (int p = begin + 4 * tid; p < end; p += kPgTile) {
         r4 = refs4(refs, p, pages);
         for (int e = 0; e < 4; ++e) used += p + e < pages && (&r4.x)[e] != 0;
     }
-    block_scan(used, &total, sums);
-    if (tid == 0) here[0] = total;
+    scan(used, &total);
+    if (tid == 0) here[0] = static_cast<int>(total);
     cluster.sync();
     int low = 0;
     for (int x = 0; x < ctas; ++x) low += cluster.map_shared_rank(here, x)[0];
@@ -293,12 +321,11 @@ __global__ void __launch_bounds__(kPgThreads) pages_plan_kernel(const int* __res
             ho += p + e < low && (&r4.x)[e] == 0;
         }
     }
-    int movers, holes;
-    block_scan(mv, &movers, sums);
-    block_scan(ho, &holes, sums);
+    // (movers, holes) are scanned in one word
+    const long long both = scan(static_cast<long long>(mv) << 32 | static_cast<unsigned>(ho), &total);
     if (tid == 0) {
-        here[1] = movers;
-        here[2] = holes;
+        here[1] = static_cast<int>(total >> 32);
+        here[2] = static_cast<int>(total);
     }
     cluster.sync();
     int mb = 0, hb = 0, all = 0;
@@ -321,10 +348,11 @@ __global__ void __launch_bounds__(kPgThreads) pages_plan_kernel(const int* __res
             ms += m[e];
             hs += h[e];
         }
-        int mt, ht;
-        int mr = mb + block_scan(ms, &mt, sums) - ms, hr = hb + block_scan(hs, &ht, sums) - hs;
-        mb += mt;
-        hb += ht;
+        long long incl = both, tile = total;               // a slice of one tile has been scanned
+        if (!one) incl = scan(static_cast<long long>(ms) << 32 | static_cast<unsigned>(hs), &tile);
+        int mr = mb + static_cast<int>(incl >> 32) - ms, hr = hb + static_cast<int>(incl) - hs;
+        mb += static_cast<int>(tile >> 32);
+        hb += static_cast<int>(tile);
         for (int e = 0; e < 4; ++e) {
             if (m[e]) {
                 from[mr] = p + e;
@@ -339,30 +367,15 @@ __global__ void __launch_bounds__(kPgThreads) pages_plan_kernel(const int* __res
         meta[0] = low;
         meta[1] = all;
     }
-    cluster.sync();
+    cluster.sync();                                    // the plan is written (and here[] read)
+    if (table) pages_follow(table, entries, refs_out, pages, from, to, rank_of, low, all);
 }
 
-// Second part: the table's entries and the counts follow the pages.
+// Second part as a launch of its own, for tables that a cluster would take long to walk.
 __global__ void __launch_bounds__(256) pages_follow_kernel(int* table, long long entries, int* refs, int pages,
-                                                           const int* __restrict__ from,
-                                                           const int* __restrict__ to,
-                                                           const int* __restrict__ rank_of,
-                                                           const int* __restrict__ meta) {
-    const int low = meta[0], all = meta[1];
-    if (all == 0) return;
-    const long long t0 = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const long long nt = static_cast<long long>(gridDim.x) * blockDim.x;
-    // a mover's rank is read only for entries that name a page in use, which is in the plan
-    for (long long i = t0; i < entries; i += nt) {
-        const int p = table[i];
-        if (p < low || p >= pages) continue;
-        const int r = rank_of[p];
-        if (r >= 0 && r < all && from[r] == p) table[i] = to[r];
-    }
-    for (long long r = t0; r < all; r += nt) {
-        refs[to[r]] = refs[from[r]];
-        refs[from[r]] = 0;
-    }
+                                                           const int* from, const int* to, const int* rank_of,
+                                                           const int* meta) {
+    pages_follow(table, entries, refs, pages, from, to, rank_of, meta[0], meta[1]);
 }
 
 // Page contents from[i] -> to[i] in every layer: pieces of up to 32 KB, one CTA at a time, eight
@@ -450,10 +463,12 @@ cudaError_t launch_pages_compact(const PageState& s, int* from, int* to, int* co
     const int cap = s.pages / 2 > 0 ? s.pages / 2 : 1;
     const int ctas = scan_ctas(s.pages);
     int* rank_of = ws + 4;
-    cudaError_t e = launch_cluster(pages_plan_kernel, ctas, 0, stream, static_cast<const int*>(s.refs), s.pages,
-                                   from, to, count, rank_of, ws, cap, ctas);
-    if (e != cudaSuccess) return e;
     const long long entries = static_cast<long long>(s.slots) * s.max_pages;
+    const bool together = entries <= 16LL * ctas * kPgThreads;       // 16 entries per thread at most
+    cudaError_t e = launch_cluster(pages_plan_kernel, ctas, 0, stream, static_cast<const int*>(s.refs), s.pages,
+                                   from, to, count, rank_of, ws, cap, ctas, together ? s.table : nullptr, entries,
+                                   s.refs);
+    if (e != cudaSuccess || together) return e;
     long long blocks = (entries + 1023) / 1024;
     blocks = blocks < 1 ? 1 : (blocks > 148 * 8 ? 148 * 8 : blocks);
     pages_follow_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(

@@ -115,22 +115,20 @@ def attn_pages_copy(pool, from_, to, count, layers, pages, page_bytes, n, stream
 def _tensors(where, *ts):
     """Packed CUDA tensors on the current device: kernels are launched there, and a host or a strided
     tensor's pointer must never reach one."""
-    dev = torch.cuda.current_device() if ts[0].is_cuda else None
+    dev = torch.cuda.current_device() if ts[0].is_cuda else -2
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda or t.get_device() != dev:
-            raise ValueError(f"{where}: tensors must be on the current CUDA device")
-        if not t.is_contiguous():
-            raise ValueError(f"{where}: tensors must be contiguous")
+        if t is not None and not (t.get_device() == dev and t.is_contiguous()):     # -1: host memory
+            raise ValueError(f"{where}: tensors must be contiguous and on the current CUDA device")
     return dev
 
 
 def _is(where, name, t, dtype, *shape):
     """t must have this dtype and shape (None: any size of that dimension)."""
-    if t.dtype != dtype or t.dim() != len(shape) or any(
-            s is not None and s != x for s, x in zip(shape, t.shape)):
-        raise ValueError(f"{where}: {name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    have = t.shape
+    if t.dtype is dtype and (have == shape or len(have) == len(shape) and all(
+            s is None or s == x for s, x in zip(shape, have))):
+        return
+    raise ValueError(f"{where}: {name} must be {dtype} {shape}, got {t.dtype} {tuple(have)}")
 
 
 def _raw_stream(stream, dev, *made):
@@ -159,11 +157,13 @@ def _page_size(where, pool, d):
 
 def _rows(where, pool, table, d, B, start, counts, seqs):
     page = _page_size(where, pool, d)
-    _is(where, "table", table, torch.int32, None, None)
+    if table.dtype is not torch.int32 or table.dim() != 2:
+        _is(where, "table", table, torch.int32, None, None)
     _is(where, "start", start, torch.int32, B)
-    for name, t in (("counts", counts), ("seqs", seqs)):
-        if t is not None:
-            _is(where, name, t, torch.int32, B)
+    if counts is not None:
+        _is(where, "counts", counts, torch.int32, B)
+    if seqs is not None:
+        _is(where, "seqs", seqs, torch.int32, B)
     return page
 
 
@@ -206,16 +206,21 @@ def kv4_gather(pool, table, start, n, d, counts=None, seqs=None, k=None, v=None,
         raise ValueError(f"{where}: n must be 1 or more")
     dev = _tensors(where, pool, table, start, counts, seqs, k, v)
     shape = (B, pool.shape[1], n, d)
-    made = [torch.empty(shape, dtype=torch.bfloat16, device=pool.device) if t is None else t for t in (k, v)]
-    for name, t in zip("kv", made):
-        _is(where, name, t, torch.bfloat16, *shape)
+    if k is None:
+        k = pool.new_empty(shape, dtype=torch.bfloat16)
+    else:
+        _is(where, "k", k, torch.bfloat16, *shape)
+    if v is None:
+        v = torch.empty_like(k)
+    else:
+        _is(where, "v", v, torch.bfloat16, *shape)
     rc = _lib.attn_kv4_gather(pool.data_ptr(), table.data_ptr(), _at(seqs), start.data_ptr(),
-                              _at(counts), made[0].data_ptr(), made[1].data_ptr(), pool.shape[0],
+                              _at(counts), k.data_ptr(), v.data_ptr(), pool.shape[0],
                               table.shape[0], table.shape[1], page, B, shape[1], n, d,
-                              _raw_stream(stream, dev, *made))
+                              _raw_stream(stream, dev, k, v))
     if rc:
         raise AttnError(rc, "attn_kv4_gather")
-    return made[0], made[1]
+    return k, v
 
 
 def kv4_attend(q, pool, table, lens, window=None, sinks=0, scale=None, seqs=None, out=None, lse=None,
@@ -233,8 +238,9 @@ def kv4_attend(q, pool, table, lens, window=None, sinks=0, scale=None, seqs=None
     pages, Hkv, _ = pool.shape
     if H % Hkv:
         raise ValueError(f"{where}: H must be a multiple of the pool's K/V heads")
-    _is(where, "q", q, torch.bfloat16, B, H, nq, d)
-    _is(where, "table", table, torch.int32, None, None)
+    if q.dtype is not torch.bfloat16 or table.dtype is not torch.int32 or table.dim() != 2:
+        _is(where, "q", q, torch.bfloat16, B, H, nq, d)
+        _is(where, "table", table, torch.int32, None, None)
     slots, width = table.shape
     _is(where, "lens", lens, torch.int32, slots)
     if seqs is not None:
@@ -244,13 +250,14 @@ def kv4_attend(q, pool, table, lens, window=None, sinks=0, scale=None, seqs=None
     dev = _tensors(where, q, pool, table, lens, seqs, out, lse, workspace)
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _is(where, "out", out, torch.bfloat16, B, H, nq, d)
     if lse is None:
-        lse = torch.empty((B, H, nq), dtype=torch.float32, device=q.device)
-    need = _lib.attn_kv4_workspace_bytes(H, Hkv, nq, d)
+        lse = q.new_empty((B, H, nq), dtype=torch.float32)
+    else:
+        _is(where, "lse", lse, torch.float32, B, H, nq)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _is(where, "out", out, torch.bfloat16, B, H, nq, d)
-    _is(where, "lse", lse, torch.float32, B, H, nq)
+        workspace = pool.new_empty(_lib.attn_kv4_workspace_bytes(H, Hkv, nq, d))
     rc = _lib.attn_kv4_attend(q.data_ptr(), pool.data_ptr(), table.data_ptr(), _at(seqs),
                               lens.data_ptr(), out.data_ptr(), lse.data_ptr(), pages, slots, width,
                               page, B, H, Hkv, nq, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
@@ -264,11 +271,13 @@ def kv4_attend(q, pool, table, lens, window=None, sinks=0, scale=None, seqs=None
 
 def _page_state(where, table, lens, refs, *ts):
     """Checks the state and the int32 vectors of one call; (pages, slots, max_pages, device)."""
-    _is(where, "table", table, torch.int32, None, None)
+    if table.dtype is not torch.int32 or table.dim() != 2:
+        _is(where, "table", table, torch.int32, None, None)
     slots, width = table.shape
     if lens is not None:
         _is(where, "lens", lens, torch.int32, slots)
-    _is(where, "refs", refs, torch.int32, None)
+    if refs.dtype is not torch.int32 or refs.dim() != 1:
+        _is(where, "refs", refs, torch.int32, None)
     for t in ts:
         _is(where, "rows and counts", t, torch.int32, ts[0].shape[0])
     return refs.shape[0], slots, width, _tensors(where, table, lens, refs, *ts)
@@ -350,7 +359,8 @@ def pages_copy(pool, frm, to, count=None, layered=False, stream=None):
     where = "pages_copy"
     if pool.dim() < (2 if layered else 1):
         raise ValueError(f"{where}: the pool needs a dimension of pages")
-    _is(where, "frm", frm, torch.int32, None)
+    if frm.dtype is not torch.int32 or frm.dim() != 1:
+        _is(where, "frm", frm, torch.int32, None)
     _is(where, "to", to, torch.int32, frm.shape[0])
     if count is not None:
         _is(where, "count", count, torch.int32, 1)
