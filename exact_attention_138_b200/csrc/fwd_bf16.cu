@@ -131,6 +131,34 @@ __device__ __forceinline__ void store_p(uint32_t* u, int c, float p0, float p1) 
     }
 }
 
+// Hides the scores u of keys that a row does not see: c < lo beyond the first `sinks`, and c > hi (all
+// relative to the tile). left, right: some row of the tile is cut on that side; apart: a sink tile
+// that lies before every row's window. Under a window every query tile has three such tiles out of ten
+// or so: one comparison per score instead of three took 219 us to 201 us (1x32x8192x128 on 8 K/V heads, window 1024, 4 sinks).
+__device__ __forceinline__ void mask_tile(uint32_t (&u)[128], int lo, int hi, int sinks, bool left, bool right,
+                                          bool apart) {
+    constexpr uint32_t kHidden = 0xff800000u;      // -inf
+    if (apart) {
+        if (left) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+                if (c >= sinks) u[c] = kHidden;
+        }
+    } else if (left && (right || sinks > 0)) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+            if ((c < lo && c >= sinks) || c > hi) u[c] = kHidden;
+    } else if (right) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+            if (c > hi) u[c] = kHidden;
+    } else if (left) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+            if (c < lo) u[c] = kHidden;
+    }
+}
+
 // SPLIT: the CTAs of a cluster share the key tiles of one tile pair (small grids); each keeps its
 // unnormalised O and (m, l) for its share, and the cluster merges them through distributed
 // shared memory with the rule that joins two softmax blocks (weights 2^(m_s - M)).
@@ -502,14 +530,14 @@ __device__ __forceinline__ void fwd_body(const CUtensorMap* tmQ_, const CUtensor
             tmem_ld_wait();
             reg_fence<128>(u);
             const int kbase = jj * C::BN;
-            const bool edge = (kbase < full_lo && (!SINK || kbase > mk.ns - C::BN)) ||
-                              kbase > full_hi;
-            if (edge) {
+            if constexpr (SINK) {
+                mask_tile(u, klo - kbase, khi - kbase, mk.ns - kbase, kbase < full_lo && kbase > mk.ns - C::BN,
+                          kbase > full_hi, t < sinks_of(g));
+            } else if (kbase < full_lo || kbase > full_hi) {
 #pragma unroll
                 for (int c = 0; c < 128; ++c) {
                     const int kidx = kbase + c;
-                    if ((kidx < klo && (!SINK || kidx >= mk.ns)) || kidx > khi)
-                        u[c] = __float_as_uint(-INFINITY);
+                    if (kidx < klo || kidx > khi) u[c] = __float_as_uint(-INFINITY);
                 }
             }
             float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
@@ -789,7 +817,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     fwd_body<D, false, true>(&tmQ, &tmK, &tmV, p);
 }
 
-// Windows with sinks, one CTA per tile pair or clusters that share its key tiles.
+// Windows with sinks, one CTA per tile pair or clusters that share its key tiles. 1x32x8192x128 on 8
+// K/V heads, window 1024, 4 sinks: 201 us. A persistent form (one CTA per SM, K/V ring, next Q and first
+// scores running on across pairs) was built and measured slower, 221 us; so was a sink step of 32 keys
+// instead of 128 (no gain).
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     fwd_bf16_sink_kernel(const __grid_constant__ CUtensorMap tmQ,
