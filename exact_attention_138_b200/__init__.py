@@ -373,6 +373,13 @@ def _sinks(sinks):
     return n
 
 
+def _current(where, t):
+    """Kernels are launched on the current device: a tensor of another one must not reach them."""
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors must be on the current CUDA device")
+
+
 def forward(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, window=None,
             sinks=0):
     """O, LSE = attention(q, k, v). q: contiguous CUDA tensor (B,H,n,d) or (n,d), bf16 or fp32;
@@ -396,6 +403,7 @@ def forward(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, 
     _shaped("forward", [(out, q.shape, q.dtype), (lse, (B, H, n) if q.dim() == 4 else (n,),
                                                   torch.float32)])
     if sinks:
+        _current("forward", q)
         wl, wr = _window(causal, window)
         rc = attn_fwd_sink(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, Hkv, n, nk, d,
                            float(scale), wl, wr, sinks, _dtype_code(q), _stream_handle(stream))
@@ -463,6 +471,7 @@ def backward(q, k, v, o, do, lse, causal=False, scale=None, deterministic=False,
                          (dk, k.shape, k.dtype), (dv, v.shape, v.dtype)])
     ws_bytes = workspace.numel() * workspace.element_size()
     if sinks:
+        _current("backward", q)
         rc = attn_bwd_sink(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
                            _ptr(dk), _ptr(dv), B, H, Hkv, n, nk, d, float(scale), wl, wr, sinks,
                            _dtype_code(q), int(bool(deterministic)), _ptr(workspace), ws_bytes,

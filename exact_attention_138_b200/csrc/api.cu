@@ -35,6 +35,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int to_code(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
@@ -176,9 +177,11 @@ unsigned attn_set_wait_timeout_us(unsigned us) {
     return g_timeout_us.exchange(us);
 }
 
-// Sinks that change the mask: none when the left bound is open, at most every key.
+// A window whose sinks are all the keys has no left bound.
+static int left_bound(int n_sink, int wl, int nk) { return wl < 0 || n_sink >= nk ? -1 : wl; }
+// Sinks that change the mask: none when the left bound is open.
 static int sinks_in_use(int n_sink, int wl, int nk) {
-    return wl < 0 ? 0 : (n_sink < nk ? n_sink : nk);
+    return left_bound(n_sink, wl, nk) < 0 ? 0 : n_sink;
 }
 
 static int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, int B,
@@ -195,7 +198,7 @@ static int fwd_impl(const void* q, const void* k, const void* v, void* o, float*
     a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
     a.B = B; a.H = H; a.nq = nq; a.nk = nk; a.d = d; a.Hkv = Hkv;
     a.scale = scale;
-    a.wl = wl < 0 ? -1 : wl;
+    a.wl = left_bound(n_sink, wl, nk);
     a.wr = wr < 0 ? -1 : wr;
     a.ns = sinks_in_use(n_sink, wl, nk);
     a.q_descale = a.k_descale = a.v_descale = 1.f;
@@ -291,10 +294,11 @@ size_t attn_bwd_workspace_bytes(int B, int H, int n, int d, int deterministic) {
 }
 
 // fp32 dK and dV partials of the key tiles that hold a sink (see BwdArgs::sink_buf).
-static size_t sink_buf_bytes(int B, int H, int Hkv, int nq, int nk, int d, int wl, int wr, int ns) {
+static size_t sink_buf_bytes(int B, int H, int Hkv, int nq, int d, int wl, int wr, int ns) {
     const size_t tiles = (static_cast<size_t>(ns) + 127) / 128;
-    return 2 * static_cast<size_t>(B) * Hkv * tiles * bwd_sink_parts(H, Hkv, nq, nk, d, wl, wr) * 128 *
-           d * sizeof(float);
+    const long long BHkv = static_cast<long long>(B) * Hkv;
+    const int parts = bwd_sink_parts(BHkv, H / Hkv, nq, d, wl, wr, ns);
+    return parts == 1 ? 0 : 2 * BHkv * tiles * parts * 128 * d * sizeof(float);
 }
 
 size_t attn_bwd_sink_workspace_bytes(int B, int H, int Hkv, int nq, int nk, int d, int window_left,
@@ -303,7 +307,7 @@ size_t attn_bwd_sink_workspace_bytes(int B, int H, int Hkv, int nq, int nk, int 
         return 0;
     const int ns = sinks_in_use(n_sink, window_left, nk);
     return ws_layout(B, H, nq, d, deterministic).total +
-           (ns > 0 ? sink_buf_bytes(B, H, Hkv, nq, nk, d, window_left, window_right, ns) : 0);
+           (ns > 0 ? sink_buf_bytes(B, H, Hkv, nq, d, window_left, window_right, ns) : 0);
 }
 
 static int bwd_impl(const void* q, const void* k, const void* v, const void* o, const void* dO,
@@ -314,21 +318,21 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* o, 
     if (rc) return rc;
     WsLayout w = ws_layout(B, H, nq, d, deterministic);
     const int ns = sinks_in_use(n_sink, wl, nk);
-    const size_t sink_bytes = ns > 0 ? sink_buf_bytes(B, H, Hkv, nq, nk, d, wl, wr, ns) : 0;
+    const size_t sink_bytes = ns > 0 ? sink_buf_bytes(B, H, Hkv, nq, d, wl, wr, ns) : 0;
     if (!workspace) return ATTN_ERR_INVALID;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_INVALID;
     if (ws_bytes < w.total + sink_bytes) return ATTN_ERR_WORKSPACE;
     BwdArgs a;
     if (ns > 0) {
         a.ns = ns;
-        a.sink_parts = bwd_sink_parts(H, Hkv, nq, nk, d, wl, wr);
+        a.sink_parts = bwd_sink_parts(static_cast<long long>(B) * Hkv, H / Hkv, nq, d, wl, wr, ns);
         a.sink_buf = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.total);
     }
     a.q = q; a.k = k; a.v = v; a.o = o; a.dO = dO; a.lse = lse;
     a.dq = dq; a.dk = dk; a.dv = dv;
     a.B = B; a.H = H; a.nq = nq; a.nk = nk; a.d = d; a.Hkv = Hkv;
     a.scale = scale;
-    a.wl = wl < 0 ? -1 : wl;
+    a.wl = n_sink > 0 ? left_bound(n_sink, wl, nk) : (wl < 0 ? -1 : wl);
     a.wr = wr < 0 ? -1 : wr;
     a.deterministic = deterministic ? 1 : 0;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -511,7 +515,7 @@ int attn_ring_accumulate(float* acc, const void* part, long long count, int part
 static int check_pool(Kv4Pool& p, const void* pool, const int* table, const int* seqs, int pages,
                       int slots, int max_pages, int page_size, int B, int Hkv, int d) {
     if (!pool || !table) return ATTN_ERR_INVALID;
-    if (!aligned16(pool)) return ATTN_ERR_INVALID;
+    if (!aligned16(pool) || !aligned4(table) || !aligned4(seqs)) return ATTN_ERR_INVALID;
     if (d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
     if (page_size < kKv4Block || page_size % kKv4Block != 0 || page_size > 65536)
         return ATTN_ERR_INVALID;
@@ -537,7 +541,8 @@ static int kv4_rows(Kv4RowsArgs& a, const void* pool, const int* table, const in
     if (!start || !k || !v) return ATTN_ERR_INVALID;
     int rc = check_pool(a.pool, pool, table, seqs, pages, slots, max_pages, page_size, B, Hkv, d);
     if (rc) return rc;
-    if (n < 1 || n > kMaxSeq || !aligned16(k) || !aligned16(v)) return ATTN_ERR_INVALID;
+    if (n < 1 || n > kMaxSeq || !aligned16(k) || !aligned16(v) || !aligned4(start) || !aligned4(counts))
+        return ATTN_ERR_INVALID;
     a.start = start;
     a.counts = counts;
     a.k = const_cast<void*>(k);
@@ -583,7 +588,7 @@ int attn_kv4_attend(const void* q, const void* pool, const int* table, const int
         return rc;
     if (H % Hkv != 0 || n_sink < 0) return ATTN_ERR_INVALID;
     if (static_cast<long long>(B) * H * nq > 0x7fffffffLL) return ATTN_ERR_INVALID;
-    if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned4(lens)) return ATTN_ERR_INVALID;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_INVALID;
     if (ws_bytes < kv4_attend_ws_bytes(H, Hkv, nq, d)) return ATTN_ERR_WORKSPACE;
     a.lens = lens;
@@ -597,8 +602,6 @@ int attn_kv4_attend(const void* q, const void* pool, const int* table, const int
     a.timeout_ns = static_cast<uint64_t>(g_timeout_us.load()) * 1000ull;
     return to_code(launch_kv4_attend(a, static_cast<cudaStream_t>(stream)));
 }
-
-static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Arguments of every call on a page table; counts of sequences are checked by the callers.
 static int check_pages(PageState& s, int* table, int* lens, int* refs, int pages, int slots,

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         visible_query_tiles(mk, j * 128LL, min(j * 128LL + 127, nk - 1LL), 128, i_begin, i_end);
     const int NT = i_end - i_begin;               // query tiles per query head
     // steps of this CTA: all query heads sharing this K/V head, or a part of them for a sink tile
-    const bool sink = SINK && j < acc.sink_nt;
+    const bool sink = SINK && j < acc.sink_nt && acc.sink_parts > 1;
     const int it0 = SINK && sink ? sink_share(acc, part, NT * p.kv_group) : 0;
     const int NTT = SINK && sink ? sink_share(acc, part + 1, NT * p.kv_group) - it0 : NT * p.kv_group;
 
@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(q64::kThreads, 1)
         visible_query_tiles(mk, j * 128LL, min(j * 128LL + 127, nk - 1LL), BQ, i_begin, i_end);
     const int NT = i_end - i_begin;               // query tiles per query head
     // steps of this CTA: all query heads sharing this K/V head, or a part of them for a sink tile
-    const bool sink = SINK && j < acc.sink_nt;
+    const bool sink = SINK && j < acc.sink_nt && acc.sink_parts > 1;
     const int it0 = SINK && sink ? sink_share(acc, part, NT * p.kv_group) : 0;
     const int NTT = SINK && sink ? sink_share(acc, part + 1, NT * p.kv_group) - it0 : NT * p.kv_group;
 
@@ -1381,7 +1381,7 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
         size_t sink_half = 0;          // floats of all dK partials
         if (a.ns > 0) {
             const int nt = sink_tiles(kp.mask, 128);
-            sink_half = static_cast<size_t>(BHkv) * nt * a.sink_parts * 128 * D;
+            if (a.sink_parts > 1) sink_half = static_cast<size_t>(BHkv) * nt * a.sink_parts * 128 * D;
             acc = AccOut{a.sink_buf, a.sink_buf + sink_half, 0, nt, a.sink_parts};
         }
         kp.scale = a.scale;
@@ -1418,7 +1418,7 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
                                                                                 acc);
         }
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        if (a.ns > 0) {
+        if (a.ns > 0 && acc.sink_parts > 1) {
             const long long rows = static_cast<long long>(acc.sink_nt) * 128;
             const int live = static_cast<int>(rows < a.nk ? rows : a.nk);
             const long long items = static_cast<long long>(BHkv) * 2 * live * (D / 4);
@@ -1445,16 +1445,18 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int bwd_sink_parts(int H, int Hkv, int nq, int nk, int d, int wl, int wr) {
+int bwd_sink_parts(long long BHkv, int kv_group, int nq, int d, int wl, int wr, int ns) {
     const int bq = d == 128 ? q64::BQ : 128;
-    const long long kvg = H / Hkv;
+    const long long kvg = kv_group;
     const long long all = ((static_cast<long long>(nq) + bq - 1) / bq) * kvg;
     // query tiles that a key tile of the window meets; an unbounded right side: half of all
     const long long span = wr < 0 ? nq / 2 : static_cast<long long>(wl) + wr + 128;
     long long each = (span / bq + 1) * kvg;
     if (each < 8) each = 8;
+    const long long tiles = BHkv * ((static_cast<long long>(ns) + 127) / 128);
+    const long long most = (8 * 148 + tiles - 1) / tiles;
     const long long parts = (all + each - 1) / each;
-    return static_cast<int>(parts < 1 ? 1 : (parts > 256 ? 256 : parts));
+    return static_cast<int>(parts < 1 ? 1 : (parts > most ? most : parts));
 }
 
 cudaError_t launch_bwd_bf16(const BwdArgs& a, cudaStream_t stream) {

@@ -158,15 +158,16 @@ struct BwdArgs {
     long long q_rows = 0, kv_rows = 0;
     int ws_rows = 0, q_row0 = 0;
     // Sinks (see MaskSpec): the queries of each key tile that holds one are shared by sink_parts
-    // CTAs, whose dK, dV partials (B·Hkv, sink tiles, parts, 128 rows, d fp32; all dK, then all dV)
-    // lie in sink_buf and are summed in a launch of their own.
+    // CTAs; if there are several, their dK, dV partials (B·Hkv, sink tiles, parts, 128 rows, d fp32; all
+    // dK, then all dV) lie in sink_buf and are summed in a launch of their own.
     int ns = 0, sink_parts = 0;
     float* sink_buf = nullptr;
 };
 
-// CTAs that share the queries of one sink key tile in the backward pass: about as many query
-// tiles each as a key tile of the window meets.
-int bwd_sink_parts(int H, int Hkv, int nq, int nk, int d, int wl, int wr);
+// CTAs that share the queries of one sink key tile in the backward pass: about as many query tiles
+// each as a key tile of the window meets, but no more than 8 per SM over all sink tiles (with that many
+// sinks the tiles themselves fill the GPU, and the partials would grow without bound).
+int bwd_sink_parts(long long BHkv, int kv_group, int nq, int d, int wl, int wr, int ns);
 
 // Encodes a 3-D tensor map over a (B*H, n, d) tensor of `esize`-byte elements (2: bf16, 1: 8-bit)
 // with a box of (chunk, box_rows, 1), chunk = min(d, 128 / esize) elements, and the swizzle that

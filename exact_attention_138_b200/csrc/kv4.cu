@@ -1105,9 +1105,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttParams 
     using C = AttCfg<D, NT>;
     constexpr int LPP = D / 4, TEAMS = kJoinThreads / LPP;
     __shared__ long long scratch[2][kJoinThreads / 32];
-    __shared__ float red[kJoinThreads / 32];
     __shared__ float4 osum[TEAMS][LPP];
-    __shared__ float lsum[TEAMS];
+    __shared__ float2 msum[TEAMS];
     const Kv4AttendArgs& a = p.a;
     const int HR = a.pool.Hkv * p.RB;
     const int b = static_cast<int>(blockIdx.x / HR), hr = static_cast<int>(blockIdx.x % HR);
@@ -1164,39 +1163,54 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttParams 
     const auto part_of = [&](int k) {
         return a.ws + (2 * static_cast<size_t>(k) + (k == r0 ? slot0 : 0)) * C::PART;
     };
-    float M = -INFINITY;
-    for (int k = r0 + static_cast<int>(threadIdx.x); k <= r1; k += kJoinThreads)
-        M = fmaxf(M, part_of(k)[C::ROWS * D + 2 * r]);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = M;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[w]);
-    float L = 0.f;
+    // each team keeps a running maximum over its parts, four of them loaded at a time; a part that saw no
+    // key has m = -inf, O = 0, and l = 0 or NaN when every score was
+    constexpr int U = 4;
+    float M = -INFINITY, L = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = r0 + team; k <= r1; k += TEAMS) {
-        const float* part = part_of(k);
-        const float2 ml = *reinterpret_cast<const float2*>(part + C::ROWS * D + 2 * r);
-        const float4 t = *reinterpret_cast<const float4*>(part + r * D + lane4 * 4);
-        // a part that saw no key has O = 0, and l = 0 or NaN when every score was
-        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-        L += ml.x == -INFINITY ? ml.y : f * ml.y;
-        v.x = fmaf(f, t.x, v.x); v.y = fmaf(f, t.y, v.y);
-        v.z = fmaf(f, t.z, v.z); v.w = fmaf(f, t.w, v.w);
+    for (int k0 = r0 + team; k0 <= r1; k0 += U * TEAMS) {
+        float2 ml[U];
+        float4 t[U];
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+            const int k = k0 + x * TEAMS;
+            const float* part = part_of(min(k, r1));
+            ml[x] = *reinterpret_cast<const float2*>(part + C::ROWS * D + 2 * r);
+            t[x] = *reinterpret_cast<const float4*>(part + r * D + lane4 * 4);
+            if (k > r1) ml[x] = make_float2(-INFINITY, 0.f);
+        }
+        float top = M;
+#pragma unroll
+        for (int x = 0; x < U; ++x) top = fmaxf(top, ml[x].x);
+        const float old = M == -INFINITY ? 0.f : ex2_approx(M - top);
+        M = top;
+        L *= M == -INFINITY ? 1.f : old;
+        v.x *= old; v.y *= old; v.z *= old; v.w *= old;
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+            const float f = ml[x].x == -INFINITY ? 0.f : ex2_approx(ml[x].x - M);
+            L += ml[x].x == -INFINITY ? ml[x].y : f * ml[x].y;
+            if (ml[x].x == -INFINITY) continue;
+            v.x = fmaf(f, t[x].x, v.x); v.y = fmaf(f, t[x].y, v.y);
+            v.z = fmaf(f, t[x].z, v.z); v.w = fmaf(f, t[x].w, v.w);
+        }
     }
     osum[team][lane4] = v;
-    if (lane4 == 0) lsum[team] = L;
+    if (lane4 == 0) msum[team] = make_float2(M, L);
     __syncthreads();
     if (team != 0) return;
+#pragma unroll
+    for (int w = 1; w < TEAMS; ++w) M = fmaxf(M, msum[w].x);
     L = 0.f;
     v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < TEAMS; ++w) {
-        L += lsum[w];
+        const float2 ml = msum[w];
+        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+        L += ml.x == -INFINITY ? ml.y : f * ml.y;
         const float4 t = osum[w][lane4];
-        v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+        v.x = fmaf(f, t.x, v.x); v.y = fmaf(f, t.y, v.y);
+        v.z = fmaf(f, t.z, v.z); v.w = fmaf(f, t.w, v.w);
     }
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
     *o = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));

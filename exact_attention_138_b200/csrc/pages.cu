@@ -433,8 +433,9 @@ template <bool FORK>
 cudaError_t launch_take(const PageState& s, const int* seqs, const int* arg, int* out0, int* out1, int n,
                         cudaStream_t stream) {
     const size_t smem = static_cast<size_t>((s.slots + 31) / 32 + 2 * n + 1) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(pages_take_kernel<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    // the bound of every call, so that two host threads never set it against each other
+    constexpr int kMost = (kPagesMaxSlots / 32 + 2 * kPagesMaxSeqs + 1) * sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(pages_take_kernel<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
     const int ctas = scan_ctas(s.pages);
     return launch_cluster(pages_take_kernel<FORK>, ctas, smem, stream, s, seqs, arg, out0, out1, n, ctas);

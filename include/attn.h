@@ -159,7 +159,7 @@ int attn_fwd_ex(const void* q, const void* k, const void* v, void* o, float* lse
  * which take much of every row's weight). Key j is visible to query i iff, with off = nk - nq,
  *     j <= i + off + window_right   and   (j >= i + off - window_left  or  j < n_sink);
  * a negative bound is none, so n_sink changes nothing when window_left is negative, and n_sink = 0
- * is attn_fwd_ex. n_sink may exceed nk. bf16 and fp32; one launch, no library memory.
+ * is attn_fwd_ex; n_sink >= nk leaves no left bound. bf16 and fp32; one launch, no library memory.
  * Errors as attn_fwd_ex; n_sink < 0 is ATTN_ERR_INVALID. */
 int attn_fwd_sink(const void* q, const void* k, const void* v, void* o, float* lse,
                   int B, int H, int Hkv, int nq, int nk, int d, float scale,
@@ -329,6 +329,8 @@ int attn_ring_accumulate(float* acc, const void* part, long long count, int part
  * attn_kv4_append: quantises rows [0, counts[i]) (NULL: n) of k, v (B, Hkv, n, d) bf16 into tokens
  *   start[i] + row. start[i] < 0 leaves the entry out; tokens on no page are dropped. No other token's
  *   bits change, nor do pages' bytes that hold no token yet. Entries of one call must not share tokens.
+ *   Pages are written whoever shares them: attn_pages_fork leaves no page shared that is still to be
+ *   written.
  * attn_kv4_gather: the same rows back as bf16(lo + s·q); rows at or beyond counts[i], of entries left
  *   out and on no page are zeros.
  * attn_kv4_attend: attn_fwd_sink of q (B, H, nq, d) bf16 over each sequence's lens[row] tokens as the

@@ -299,7 +299,7 @@ def _attend_code(**kw):
     (dict(ws=0), 1), (dict(ws=FAKE + 16), 1), (dict(pool=FAKE + 8), 1), (dict(q=FAKE + 2), 1), (dict(page=8), 1),
     (dict(page=24), 1), (dict(pages=0), 1), (dict(slots=0), 1), (dict(width=0), 1), (dict(B=0), 1), (dict(B=3), 1),
     (dict(B=70000, seqs=FAKE), 1), (dict(H=3), 1), (dict(Hkv=0), 1), (dict(nq=0), 1), (dict(scale=0.0), 1),
-    (dict(ns=-1), 1), (dict(width=1 << 28), 1), (dict(d=48), 2), (dict(bytes=100), 5)])
+    (dict(ns=-1), 1), (dict(lens=FAKE + 2), 1), (dict(table=FAKE + 1), 1), (dict(seqs=FAKE + 2), 1), (dict(width=1 << 28), 1), (dict(d=48), 2), (dict(bytes=100), 5)])
 def test_attend_refusals(kw, code):
     assert _attend_code(**kw) == code
 

@@ -30,6 +30,8 @@ CASES = [
     (1, 2, 2, 300, 300, 64, -1, 0, 7),             # open window: sinks change nothing
     (1, 40, 8, 2000, 2000, 128, 300, 0, 4),        # fills the GPU: no key split
     (1, 40, 40, 1300, 1300, 64, 129, 0, 70),
+    (1, 2, 1, 700, 3000, 128, 30, 0, 2900),        # so many sink tiles that none is shared
+    (2, 20, 20, 640, 1100, 64, 64, 0, 1099),       # one part per sink tile
 ]
 
 
@@ -185,15 +187,25 @@ def test_refusals(kw, code):
                             a["scale"], 10, 0, a["ns"], a["dtype"], 0, p(), 1 << 40, None) == code
 
 
+def test_workspace_of_many_sinks_stays_bounded():
+    # partials: at most 8 x 148 + one per sink tile of 128 rows, K and V, fp32; none without parts
+    for ns in (1, 4000, 60000, 131071, 131072):
+        extra = (ea.attn_bwd_sink_workspace_bytes(1, 8, 8, 131072, 131072, 128, 1024, 0, ns, 0)
+                 - ea.attn_bwd_workspace_bytes(1, 8, 131072, 128, 0))
+        tiles = 8 * -(-ns // 128)
+        assert 0 <= extra <= (8 * 148 + tiles) * 2 * 128 * 128 * 4
+        assert (extra == 0) == (ns >= 131072 or tiles >= 8 * 148)
+
+
 def test_backward_refuses_a_small_workspace_and_fp32():
     p = ctypes.c_void_p(FAKE)
-    need = ea.attn_bwd_sink_workspace_bytes(1, 2, 2, 100, 100, 64, 10, 0, 4, 0)
-    assert need > ea.attn_bwd_workspace_bytes(1, 2, 100, 64, 0)
-    call = lambda dt, n: ea.attn_bwd_sink(*[p] * 9, 1, 2, 2, 100, 100, 64, 0.1, 10, 0, 4, dt, 0, p,  # noqa: E731
+    need = ea.attn_bwd_sink_workspace_bytes(1, 2, 2, 5000, 5000, 64, 10, 0, 4, 0)
+    assert need > ea.attn_bwd_workspace_bytes(1, 2, 5000, 64, 0)
+    call = lambda dt, n: ea.attn_bwd_sink(*[p] * 9, 1, 2, 2, 5000, 5000, 64, 0.1, 10, 0, 4, dt, 0, p,  # noqa: E731
                                           n, None)
     assert call(ea.ATTN_BF16, need - 1) == ea.ATTN_ERR_WORKSPACE
     assert call(ea.ATTN_FP32, need) == ea.ATTN_ERR_UNSUPPORTED
-    assert ea.attn_bwd_sink_workspace_bytes(1, 2, 2, 100, 100, 64, 10, 0, -1, 0) == 0
+    assert ea.attn_bwd_sink_workspace_bytes(1, 2, 2, 5000, 5000, 64, 10, 0, -1, 0) == 0
 
 
 @pytest.mark.parametrize("bad", [-1, 1.5, 1 << 31])
