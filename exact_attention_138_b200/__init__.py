@@ -66,6 +66,9 @@ _ll = ctypes.c_longlong
 _lib.attn_fwd_fp8.restype = _i
 _lib.attn_fwd_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _i, _f, _f,
                               _f, _vp]
+_lib.attn_fwd_fp8_sink.restype = _i
+_lib.attn_fwd_fp8_sink.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _i, _i,
+                                   _f, _f, _f, _vp]
 _lib.attn_ring_merge.restype = _i
 _lib.attn_ring_merge.argtypes = [_vp, _vp, _vp, _vp, _ll, _i, _i, _i, _vp, _i, _vp]
 _lib.attn_ring_accumulate.restype = _i
@@ -172,6 +175,12 @@ def attn_fwd_fp8(q, k, v, o, lse, B, H, Hkv, nq, nk, d, scale, window_left, wind
                  q_descale, k_descale, v_descale, stream) -> int:
     return _lib.attn_fwd_fp8(q, k, v, o, lse, B, H, Hkv, nq, nk, d, scale, window_left,
                              window_right, q_descale, k_descale, v_descale, stream)
+
+
+def attn_fwd_fp8_sink(q, k, v, o, lse, B, H, Hkv, nq, nk, d, scale, window_left, window_right, n_sink,
+                      q_descale, k_descale, v_descale, stream) -> int:
+    return _lib.attn_fwd_fp8_sink(q, k, v, o, lse, B, H, Hkv, nq, nk, d, scale, window_left,
+                                  window_right, n_sink, q_descale, k_descale, v_descale, stream)
 
 
 def attn_ring_merge(o_acc, lse_acc, o_part, lse_part, rows, d, part_dtype, first, o_out,
@@ -602,7 +611,7 @@ def ring_accumulate(acc, part=None, first=False, out=None, stream=None):
 
 
 def forward_fp8(q, k, v, q_descale=1.0, k_descale=1.0, v_descale=1.0, causal=False, scale=None,
-                out=None, lse=None, stream=None, window=None):
+                out=None, lse=None, stream=None, window=None, sinks=0):
     """O (bf16), LSE of attention with E4M3 inputs: q, k, v are torch.float8_e4m3fn (or uint8
     holding E4M3 bytes) CUDA tensors (B,H,nq,d) / (B,Hkv,nk,d), d in {64, 128}; the real inputs
     are q·q_descale, k·k_descale, v·v_descale. Masks as `forward`."""
@@ -615,6 +624,7 @@ def forward_fp8(q, k, v, q_descale=1.0, k_descale=1.0, v_descale=1.0, causal=Fal
     if v.shape != k.shape or kd[0] != B or kd[3] != d or H % kd[1] != 0:
         raise ValueError("k, v must be (B, Hkv, nk, d) with H a multiple of Hkv")
     Hkv, nk = kd[1], kd[2]
+    sinks = _sinks(sinks)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
@@ -625,9 +635,11 @@ def forward_fp8(q, k, v, q_descale=1.0, k_descale=1.0, v_descale=1.0, causal=Fal
     _shaped("forward_fp8", [(out, q.shape, torch.bfloat16),
                             (lse, (B, H, n) if q.dim() == 4 else (n,), torch.float32)])
     wl, wr = _window(causal, window)
-    rc = attn_fwd_fp8(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, Hkv, n, nk, d,
-                      float(scale), wl, wr, float(q_descale), float(k_descale), float(v_descale),
-                      _stream_handle(stream))
+    if sinks:
+        _current("forward_fp8", q)
+    rc = attn_fwd_fp8_sink(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, Hkv, n, nk, d,
+                           float(scale), wl, wr, sinks, float(q_descale), float(k_descale),
+                           float(v_descale), _stream_handle(stream))
     _check(rc, "attn_fwd_fp8")
     return out, lse
 

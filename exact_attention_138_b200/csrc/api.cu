@@ -198,7 +198,7 @@ static int fwd_impl(const void* q, const void* k, const void* v, void* o, float*
     a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
     a.B = B; a.H = H; a.nq = nq; a.nk = nk; a.d = d; a.Hkv = Hkv;
     a.scale = scale;
-    a.wl = left_bound(n_sink, wl, nk);
+    a.wl = n_sink > 0 ? left_bound(n_sink, wl, nk) : (wl < 0 ? -1 : wl);
     a.wr = wr < 0 ? -1 : wr;
     a.ns = sinks_in_use(n_sink, wl, nk);
     a.q_descale = a.k_descale = a.v_descale = 1.f;
@@ -265,11 +265,19 @@ int attn_fwd_accumulate(const void* q, const void* k, const void* v, float* o_ac
 int attn_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
                  int Hkv, int nq, int nk, int d, float scale, int window_left, int window_right,
                  float q_descale, float k_descale, float v_descale, void* stream) {
+    return attn_fwd_fp8_sink(q, k, v, o, lse, B, H, Hkv, nq, nk, d, scale, window_left, window_right,
+                             0, q_descale, k_descale, v_descale, stream);
+}
+
+int attn_fwd_fp8_sink(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                      int H, int Hkv, int nq, int nk, int d, float scale, int window_left,
+                      int window_right, int n_sink, float q_descale, float k_descale,
+                      float v_descale, void* stream) {
     if (!q || !k || !v || !o || !lse) return ATTN_ERR_INVALID;
     int rc = validate_common(B, H, nq, d, scale, ATTN_BF16);
     if (rc) return rc;
     if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
-    if (nk < 1 || nk > kMaxSeq || Hkv < 1 || H % Hkv != 0) return ATTN_ERR_INVALID;
+    if (nk < 1 || nk > kMaxSeq || Hkv < 1 || H % Hkv != 0 || n_sink < 0) return ATTN_ERR_INVALID;
     const float ds[3] = {q_descale, k_descale, v_descale};
     for (float x : ds)
         if (!(x > 0.f) || !isfinite(x)) return ATTN_ERR_INVALID;
@@ -279,8 +287,9 @@ int attn_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* ls
     a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
     a.B = B; a.H = H; a.nq = nq; a.nk = nk; a.d = d; a.Hkv = Hkv;
     a.scale = scale;
-    a.wl = window_left < 0 ? -1 : window_left;
+    a.wl = n_sink > 0 ? left_bound(n_sink, window_left, nk) : (window_left < 0 ? -1 : window_left);
     a.wr = window_right < 0 ? -1 : window_right;
+    a.ns = sinks_in_use(n_sink, window_left, nk);
     a.q_descale = q_descale;
     a.k_descale = k_descale;
     a.v_descale = v_descale;

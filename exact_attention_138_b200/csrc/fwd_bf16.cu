@@ -837,6 +837,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     fwd_body<D, true, false>(&tmQ, &tmK, &tmV, p);
 }
 
+// E4M3 inputs under windows with sinks.
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    fwd_fp8_sink_kernel(const __grid_constant__ CUtensorMap tmQ,
+                        const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const FwdKParams p) {
+    fwd_body<D, true, SPLIT, false, true>(&tmQ, &tmK, &tmV, p);
+}
+
 // E4M3 inputs on small grids: clusters of p.split CTAs as fwd_bf16_split_kernel.
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -945,7 +954,7 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t stream) {
     if ((e = make_tmap(&mk, a.k, esize, BHkv, a.nk, D, 128, a.kv_rows)) != cudaSuccess) return e;
     if ((e = make_tmap(&mv, a.v, esize, BHkv, a.nk, D, 128, a.kv_rows)) != cudaSuccess) return e;
     void (*kern)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const FwdKParams);
-    if constexpr (F8) kern = fwd_fp8_kernel<D>;
+    if constexpr (F8) kern = a.ns > 0 ? fwd_fp8_sink_kernel<D, false> : fwd_fp8_kernel<D>;
     else kern = a.ns > 0 ? fwd_bf16_sink_kernel<D, false> : fwd_bf16_kernel<D>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
@@ -988,8 +997,10 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t stream) {
         return cudaGetLastError();
     }
     auto skern = split_kernel<D, F8>();
-    if constexpr (!F8)
-        if (a.ns > 0) skern = fwd_bf16_sink_kernel<D, true>;
+    if (a.ns > 0) {
+        if constexpr (F8) skern = fwd_fp8_sink_kernel<D, true>;
+        else skern = fwd_bf16_sink_kernel<D, true>;
+    }
     e = cudaFuncSetAttribute(skern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_SPLIT);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

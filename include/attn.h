@@ -165,6 +165,12 @@ int attn_fwd_sink(const void* q, const void* k, const void* v, void* o, float* l
                   int B, int H, int Hkv, int nq, int nk, int d, float scale,
                   int window_left, int window_right, int n_sink, int dtype, void* stream);
 
+/* The same mask with E4M3 inputs: attn_fwd_fp8 with n_sink; other arguments, numerics and errors as there. */
+int attn_fwd_fp8_sink(const void* q, const void* k, const void* v, void* o, float* lse,
+                      int B, int H, int Hkv, int nq, int nk, int d, float scale,
+                      int window_left, int window_right, int n_sink,
+                      float q_descale, float k_descale, float v_descale, void* stream);
+
 /* Backward pass (bf16 only). Inputs q, k, v, o, dO (bf16) and lse (fp32, from attn_fwd with the
  * same scale and causal flag). Writes dq, dk, dv (bf16). The workspace (caller-owned device
  * memory of at least attn_bwd_workspace_bytes() bytes, 256-byte aligned) is overwritten.

@@ -87,6 +87,26 @@ def test_forward_fp32(cuda_device, case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", [c for c in CASES if c[5] > 32], ids=_ids)
+def test_forward_fp8(cuda_device, case):
+    # each weight is rounded to E4M3: by 2^-4 of itself at most, or by 2^-10 where it is below 2^-6 of a
+    # reference that is at most the row's largest (so by 2^-10 max(p) of the normalised weights); scores
+    # are exact in fp32, so LSE keeps the bf16 path's bound
+    q, k, v, _ = (x.to(torch.float8_e4m3fn) for x in _inputs(case, torch.float32))
+    vis = ref.visible(*case[3:5], *case[6:])
+    o, lse = ea.forward_fp8(q.cuda(), k.cuda(), v.cuda(), v_descale=0.5, window=case[6:8], sinks=case[8])
+    assert ea.device_status() == ea.ATTN_OK
+    q, k, v = (ref.f64(x.float()) for x in (q, k, v))
+    v = v * 0.5
+    p, rlse = ref.probabilities(q, k, vis, ref.default_scale(case[5]))
+    ve = ref._expand(v, case[1])
+    ro = p @ ve
+    bound = 2.0 ** -4 * (p @ np.abs(ve)) + 2.0 ** -10 * p.max(-1, keepdims=True) * (vis.astype(float) @ np.abs(ve))
+    _close(o, ro, (bound + ref.BF16 * np.abs(ro)) * 1.02 + 1e-6, "o")
+    _close_lse(lse, rlse, TOL_LSE["bf16"])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("det", [False, True])
 @pytest.mark.parametrize("case", CASES, ids=_ids)
 def test_backward(cuda_device, case, det):
@@ -183,6 +203,9 @@ def test_refusals(kw, code):
     p = lambda x=FAKE: ctypes.c_void_p(x)                                # noqa: E731
     assert ea.attn_fwd_sink(p(a["q"]), p(), p(), p(), p(), 1, a["H"], a["Hkv"], 100, a["nk"], a["d"],
                             a["scale"], 10, 0, a["ns"], a["dtype"], None) == code
+    if "dtype" not in kw:
+        assert ea.attn_fwd_fp8_sink(p(a["q"]), p(), p(), p(), p(), 1, a["H"], a["Hkv"], 100, a["nk"], a["d"],
+                                    a["scale"], 10, 0, a["ns"], 1.0, 1.0, 1.0, None) == code
     assert ea.attn_bwd_sink(p(a["q"]), *[p()] * 8, 1, a["H"], a["Hkv"], 100, a["nk"], a["d"],
                             a["scale"], 10, 0, a["ns"], a["dtype"], 0, p(), 1 << 40, None) == code
 
