@@ -21,13 +21,14 @@
 //                   bf16) | dP^T, dQ double-buffered so the next tile's MMAs never wait for it.
 //   bwd_main_q64    (d = 128) see below.
 //   bwd_dq_convert  dQ = scale·acc -> bf16.                                    HBM-bound
+//                   (with sinks, bwd_sink_finish: this and the sum of their dK, dV parts)
 // Masks (causal, sliding window, query/key lengths that differ; see MaskSpec): key tile j only
 // meets the query tiles that hold a query which sees one of its keys; a key tile that no query
 // sees gets dK = dV = 0.
 // Sinks (MaskSpec::ns, the SINK kernels): a key tile that holds a sink meets every later query tile,
 // nq/(window + 128) times the work of the others, and would run on alone at the end. Its query
 // tiles are shared by sink_parts CTAs, each about as long as a window tile's; every one stores its dK,
-// dV partial in fp32, and bwd_sink_sum adds the parts in a fixed order. dQ needs nothing of its own:
+// dV partial in fp32, and bwd_sink_finish adds the parts in a fixed order. dQ needs nothing of its own:
 // the partial of a (query tile, key tile) pair still comes from exactly one CTA.
 #include "kernels.h"
 #include "sm100_ptx.cuh"
@@ -214,13 +215,12 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __nv_bfloat16
 // dQ = scale · acc, rounded to bf16.
 // ------------------------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(256) bwd_dq_convert_kernel(const float* __restrict__ dq_acc,
-                                                             __nv_bfloat16* __restrict__ dq, int n,
-                                                             int n_pad, long long total8,
-                                                             float scale) {
+__device__ __forceinline__ void dq_convert(const float* __restrict__ dq_acc,
+                                           __nv_bfloat16* __restrict__ dq, int n, int n_pad,
+                                           long long total8, float scale, int block, int blocks) {
     constexpr int G = D / 8;   // groups of 8 elements per row
-    for (long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; t < total8;
-         t += static_cast<long long>(gridDim.x) * blockDim.x) {
+    for (long long t = static_cast<long long>(block) * blockDim.x + threadIdx.x; t < total8;
+         t += static_cast<long long>(blocks) * blockDim.x) {
         const long long row = t / G;           // (bh, q) in unpadded space
         const int part = static_cast<int>(t % G);
         const long long bh = row / n;
@@ -236,34 +236,58 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_kernel(const float* __rest
     }
 }
 
-// ------------------------------------------------------------------------------------------
-// dK, dV of the key tiles that hold a sink: the sum of their parts in order, rounded to bf16.
-// One thread per 4 channels of a key row and of dK or dV; the parts of a row lie 128·D floats apart.
-// ------------------------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const float* __restrict__ part,
-                                                           __nv_bfloat16* __restrict__ dk,
-                                                           __nv_bfloat16* __restrict__ dv, int nk,
-                                                           int nt, int parts, int rows,
-                                                           long long items, size_t dv_off) {
+__global__ void __launch_bounds__(256) bwd_dq_convert_kernel(const float* __restrict__ dq_acc,
+                                                             __nv_bfloat16* __restrict__ dq, int n,
+                                                             int n_pad, long long total8,
+                                                             float scale) {
+    dq_convert<D>(dq_acc, dq, n, n_pad, total8, scale, blockIdx.x, gridDim.x);
+}
+
+// ------------------------------------------------------------------------------------------
+// Sinks: dK, dV of the key tiles that hold one are the sum of their parts, in order, rounded to bf16, made
+// in the launch of the dQ conversion: both only wait for the main kernel, so a launch of its own would
+// add its latency. Forward and backward together, with two launches and with one: 63.3 and 61.6 us for
+// 2x6 heads on 2x2, 777 queries on 1031 keys, d 64, 130 sinks; 688 and 685 us for 1x32 on 8 heads, 8192
+// queries and keys, d 128, 4 sinks.
+// Blocks [0, SinkSum::blocks) sum: a thread per 4 channels of a key row of dK or dV; the parts of a row
+// lie 128·D floats apart. The other blocks convert.
+// ------------------------------------------------------------------------------------------
+struct SinkSum {
+    const float* part;
+    __nv_bfloat16* dk;
+    __nv_bfloat16* dv;
+    int nk, nt, parts, rows;      // key rows, sink tiles, parts of each, key rows that they hold
+    long long items;
+    size_t dv_off;
+    int blocks;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) bwd_sink_finish_kernel(const float* __restrict__ dq_acc,
+                                                              __nv_bfloat16* __restrict__ dq, int n, int n_pad,
+                                                              long long total8, float scale, const SinkSum s) {
     constexpr int G = D / 4;
-    for (long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; t < items;
-         t += static_cast<long long>(gridDim.x) * blockDim.x) {
+    if (static_cast<int>(blockIdx.x) >= s.blocks) {
+        dq_convert<D>(dq_acc, dq, n, n_pad, total8, scale, blockIdx.x - s.blocks, gridDim.x - s.blocks);
+        return;
+    }
+    for (long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; t < s.items;
+         t += static_cast<long long>(s.blocks) * blockDim.x) {
         const int g = static_cast<int>(t % G);
         const long long r = t / G;                    // (K/V head, dK or dV, key row)
-        const int key = static_cast<int>(r % rows);
-        const int which = static_cast<int>(r / rows % 2);
-        const long long kvbh = r / rows / 2;
-        const float* src = part + (which ? dv_off : 0) +
-                           (static_cast<size_t>(kvbh * nt + key / 128) * parts * 128 + key % 128) * D +
-                           g * 4;
+        const int key = static_cast<int>(r % s.rows);
+        const int which = static_cast<int>(r / s.rows % 2);
+        const long long kvbh = r / s.rows / 2;
+        const float* src = s.part + (which ? s.dv_off : 0) +
+                           (static_cast<size_t>(kvbh * s.nt + key / 128) * s.parts * 128 + key % 128) * D + g * 4;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int x = 0; x < parts; ++x) {
+        for (int x = 0; x < s.parts; ++x) {
             const float4 b = *reinterpret_cast<const float4*>(src + static_cast<size_t>(x) * 128 * D);
             a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
         }
-        *reinterpret_cast<uint2*>((which ? dv : dk) + (static_cast<size_t>(kvbh) * nk + key) * D + g * 4) =
+        *reinterpret_cast<uint2*>((which ? s.dv : s.dk) + (static_cast<size_t>(kvbh) * s.nk + key) * D + g * 4) =
             make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
     }
 }
@@ -1352,6 +1376,7 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
             n_sems);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
+    SinkSum sum = {};
     // 2. main
     if (a.phases & 2) {
         if (a.deterministic && !(a.phases & 1)) {
@@ -1420,13 +1445,11 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if (a.ns > 0 && acc.sink_parts > 1) {
             const long long rows = static_cast<long long>(acc.sink_nt) * 128;
-            const int live = static_cast<int>(rows < a.nk ? rows : a.nk);
-            const long long items = static_cast<long long>(BHkv) * 2 * live * (D / 4);
-            long long blocks = (items + 255) / 256;
-            if (blocks > 148 * 16) blocks = 148 * 16;
-            bwd_sink_sum_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-                a.sink_buf, kp.dk, kp.dv, a.nk, acc.sink_nt, acc.sink_parts, live, items, sink_half);
-            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            sum = SinkSum{a.sink_buf, kp.dk, kp.dv, a.nk, acc.sink_nt, acc.sink_parts,
+                          static_cast<int>(rows < a.nk ? rows : a.nk), 0, sink_half, 0};
+            sum.items = static_cast<long long>(BHkv) * 2 * sum.rows * (D / 4);
+            const long long blocks = (sum.items + 255) / 256;
+            sum.blocks = static_cast<int>(blocks < 148 * 4 ? blocks : 148 * 4);
         }
         if (ev && ev[2] && (e = cudaEventRecord(ev[2], stream)) != cudaSuccess) return e;
     }
@@ -1435,8 +1458,12 @@ cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t stream) {
         const long long total8 = static_cast<long long>(BH) * a.nq * (D / 8);
         long long blocks = (total8 + 255) / 256;
         if (blocks > 148 * 16) blocks = 148 * 16;
-        bwd_dq_convert_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-            a.dq_acc, static_cast<__nv_bfloat16*>(a.dq), a.nq, n_pad, total8, a.scale);
+        if (sum.blocks > 0)      // (sinks: all three phases run in one call)
+            bwd_sink_finish_kernel<D><<<static_cast<unsigned>(blocks + sum.blocks), 256, 0, stream>>>(
+                a.dq_acc, static_cast<__nv_bfloat16*>(a.dq), a.nq, n_pad, total8, a.scale, sum);
+        else
+            bwd_dq_convert_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+                a.dq_acc, static_cast<__nv_bfloat16*>(a.dq), a.nq, n_pad, total8, a.scale);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if (ev && ev[3] && (e = cudaEventRecord(ev[3], stream)) != cudaSuccess) return e;
     }

@@ -134,7 +134,8 @@ __device__ __forceinline__ void store_p(uint32_t* u, int c, float p0, float p1) 
 // Hides the scores u of keys that a row does not see: c < lo beyond the first `sinks`, and c > hi (all
 // relative to the tile). left, right: some row of the tile is cut on that side; apart: a sink tile
 // that lies before every row's window. Under a window every query tile has three such tiles out of ten
-// or so: one comparison per score instead of three took 219 us to 201 us (1x32x8192x128 on 8 K/V heads, window 1024, 4 sinks).
+// or so: one comparison per score instead of three took 219 us to 201 us (1x32x8192x128 on 8 K/V heads,
+// window 1024, 4 sinks).
 __device__ __forceinline__ void mask_tile(uint32_t (&u)[128], int lo, int hi, int sinks, bool left, bool right,
                                           bool apart) {
     constexpr uint32_t kHidden = 0xff800000u;      // -inf

@@ -359,8 +359,9 @@ __device__ __forceinline__ long long att_scan(long long v, long long* all, long 
 
 // The line that is cut into runs: segment after segment, each kAttSwitch places for beginning it (a
 // CTA that holds many short segments would finish last otherwise: 64 sequences of 1 to 8192 tokens
-// took 112 us without, 103, 89, 87 and 89 us with 1, 3, 4 and 6 places) and one place per tile. Where runs are short anyway, the
-// switches are not counted. (tiles, segments) of the entries below one are summed in one word.
+// took 112 us without, 103, 89, 87 and 89 us with 1, 3, 4 and 6 places) and one place per tile. Where
+// runs are short anyway, the switches are not counted. (tiles, segments) of the entries below one are
+// summed in one word.
 constexpr int kAttSwitch = 4;
 __device__ __forceinline__ long long att_pair(const AttSeq& s, int tile) {
     return s.nb > 0 ? static_cast<long long>(att_tiles(s, tile)) << 16 | 1 : 0;
