@@ -51,6 +51,39 @@ APPENDS = [
 ]
 
 
+def _scale_ties(sign):
+    """(32, 32) bf16: groups whose range is 15 m for odd m of 9 bits, so that a 15th of it lies midway
+    between two bf16 values. Greatest and least have 8 bits at most."""
+    rows = []
+    for i in range(32):
+        m = 2 * (128 + 4 * i + i % 4) + 1                    # 9 bits, odd
+        width = 15 * m
+        step = 16 if width < 4096 else 32
+        hi, lo = width // step * step, -(width % step)
+        between = [lo + (hi - lo) * (x + 0.5) / 30 for x in range(30)]
+        rows.append([hi, lo] + between)
+    return sign * torch.tensor(rows).bfloat16()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sign", [1, -1])
+def test_append_rounds_exact_ties_of_the_scale_to_even(cuda_device, sign):
+    k = _scale_ties(sign)
+    x = ref.f64(k)
+    fifteenth = (x.max(-1) - x.min(-1)) / 15
+    s = ref.quantise(x)[1][:, 0]
+    other = 2 * fifteenth - s                                # the neighbour that is as near
+    assert (s != other).all() and np.array_equal(ref.bf16(other), other)
+    k = k.view(1, 1, 32, 32)
+    pool = torch.zeros((2, 1, 20 * 32), dtype=torch.uint8)
+    want = pool.numpy().copy()
+    for t in range(32):
+        ref.store(want, t // 16, 0, t % 16, ref.f64(k[0, 0, t]), ref.f64(k[0, 0, t]))
+    dev = pool.cuda()
+    ea.kv4_append(dev, _i32([[0, 1]]), _i32([0]), k.cuda(), k.cuda())
+    assert np.array_equal(dev.cpu().numpy(), want)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("case", APPENDS, ids=str)
 def test_append_writes_exactly_its_tokens(cuda_device, case):
