@@ -342,6 +342,8 @@ int attn_ring_accumulate(float* acc, const void* part, long long count, int part
  * attn_kv4_attend: attn_fwd_sink of q (B, H, nq, d) bf16 over each sequence's lens[row] tokens as the
  *   cache holds them, for the few newest tokens: query t sits at key position lens - nq + t, and
  *     j <= lens - nq + t + window_right and (j >= lens - nq + t - window_left or j < n_sink).
+ *   Products are fp32 sums. Q is held in fp16 under a power of two of each row's (exact down to 2^-27 of
+ *   the row's largest |q|, errors of 2^-35 of it below), P·s likewise (2^-11, or 2^-27 of the largest).
  *   Tokens on no page are not seen (so pages that a window has left behind can be freed). o (B, H, nq,
  *   d) bf16, lse (B, H, nq) fp32; a row that sees no key gets o = 0, lse = -inf. Any nq >= 1 is computed,
  *   8 (or 16) query rows of a K/V head share one pass over its keys. lens is read on the device:
