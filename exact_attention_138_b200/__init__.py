@@ -573,7 +573,8 @@ class BackwardSum:
 
 
 def device_status(stream=None) -> int:
-    """Synchronise and return/clear the device status word (ATTN_OK or ATTN_ERR_TIMEOUT)."""
+    """Synchronise and return/clear the device status (ATTN_OK, ATTN_ERR_TIMEOUT, or ATTN_ERR_PAGES if a
+    page call was refused; of both, the fault first, the refusal with the next call)."""
     return attn_get_device_status(_stream_handle(stream))
 
 

@@ -698,12 +698,14 @@ void attn_set_bwd_phase_events(void* const* events) {
 int attn_get_device_status(void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;
+    // a fault before a refusal; the word that is reported is cleared, the other one waits for the next call
+    const int zero = 0;
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
-    if (v != 0) {
-        const int zero = 0;
-        if (cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
-    }
+    if (v != 0)
+        return cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) == cudaSuccess ? v : ATTN_ERR_CUDA;
+    if (cudaMemcpyFromSymbol(&v, g_refused, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (v != 0 && cudaMemcpyToSymbol(g_refused, &zero, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
     return v;
 }
 

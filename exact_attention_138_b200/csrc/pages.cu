@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kPgThreads) pages_take_kernel(const PageState 
                 if (!refused) s.lens[seqs[i]] = len[i] + arg[i];
             }
         }
-        if (refused && tid == 0) report_error(kErrPages);
+        if (refused && tid == 0) report_refusal(kErrPages);
     }
     cluster.sync();                                    // free_here may still be read by a neighbour
 }
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const PageState s, cons
                                                          int whole, int wl, int ns) {
     const int q = seqs[blockIdx.x];
     if (q < 0 || q >= s.slots) {
-        if (threadIdx.x == 0) report_error(kErrPages);
+        if (threadIdx.x == 0) report_refusal(kErrPages);
         return;
     }
     const long long cap = static_cast<long long>(s.max_pages) * s.page_size;

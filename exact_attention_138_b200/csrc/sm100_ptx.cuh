@@ -12,11 +12,13 @@
 namespace attn {
 
 // ------------------------------------------------------------------------------------------
-// Device status word and bounded waits
+// Device status words and bounded waits
 // ------------------------------------------------------------------------------------------
-// g_status is sticky: the first error code written stays until the host reads and clears it.
-// (libattn.cu is the only translation unit, so the definition lives here.)
+// g_status is sticky: the first error code written stays until the host reads and clears it. A refused
+// page call, which is no fault, has a word of its own, so that neither hides the other.
+// (libattn.cu is the only translation unit, so the definitions live here.)
 __device__ int g_status = 0;
+__device__ int g_refused = 0;
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;
@@ -25,6 +27,7 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 }
 
 __device__ __forceinline__ void report_error(int code) { atomicCAS(&g_status, 0, code); }
+__device__ __forceinline__ void report_refusal(int code) { atomicCAS(&g_refused, 0, code); }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

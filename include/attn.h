@@ -273,9 +273,11 @@ int attn_bwd_accumulate(const void* q, const void* k, const void* v, const void*
 int attn_bwd_finish(void* dq, int B, int H, int nq, int d, float scale, int dtype,
                     int deterministic, void* workspace, size_t ws_bytes, void* stream);
 
-/* Synchronises `stream`, then returns and clears the sticky device status word: ATTN_OK, or
+/* Synchronises `stream`, then returns and clears the sticky device status: ATTN_OK, or
  * ATTN_ERR_TIMEOUT if a kernel's bounded wait expired since the last call, or ATTN_ERR_CUDA if
- * the synchronisation itself failed. */
+ * the synchronisation itself failed, or ATTN_ERR_PAGES if a page call was refused. A fault and a refusal
+ * are kept apart: of both, one call returns and clears the fault, the next the refusal. The status is one
+ * per device, of all streams: which call was refused is told by its results of -1. */
 int attn_get_device_status(void* stream);
 
 /* Sets the limit of every device-side wait, in microseconds (default 2,000,000 = 2 s). Values
