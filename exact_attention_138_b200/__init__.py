@@ -13,6 +13,8 @@ Raw entry points keep the C names (``attn_fwd``, ``attn_fwd_gqa``, ``attn_fwd_ex
 ``attn_bwd_gqa``, ``attn_bwd_ex``, ``attn_bwd_workspace_bytes``,
 ``attn_get_device_status``, ``attn_set_wait_timeout_us``, ``attn_selftest_wait_timeout``,
 ``attn_error_string``, ``attn_version``); ``forward`` / ``backward`` wrap them for torch tensors.
+``stream=`` (a torch CUDA stream; the current one without it) is where a call runs: the caller orders
+it after what makes the inputs, and before what reads the results; the inputs live until it is done.
 """
 from __future__ import annotations
 
@@ -281,6 +283,33 @@ def _stream_handle(stream):
     return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
+def _torch_stream(stream):
+    import torch
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
+
+
+def _fill(stream, *pairs):
+    """(tensor or None, make) pairs -> the tensors, made where there is none, for a call on `stream`. The
+    caching allocator orders a block's uses only on the stream it was allocated for: made on the current
+    stream, a block for another one could still be in use by what the current stream has queued, and
+    would be handed out again, once dropped, while the call still uses it. So such tensors are allocated
+    on `stream`, and are not reused before the current stream, on which the caller may read them, has passed
+    the point where they are dropped."""
+    import torch
+    if stream is None or all(t is not None for t, _ in pairs) or \
+            stream.cuda_stream == torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()):
+        return [make() if t is None else t for t, make in pairs]
+    now = torch.cuda.current_stream()
+    out = []
+    with torch.cuda.stream(_torch_stream(stream)):
+        for t, make in pairs:
+            if t is None:
+                t = make()
+                t.record_stream(now)
+            out.append(t)
+    return out
+
+
 def _head_rows(*ts):
     """Rows between consecutive heads shared by (B, H, n, d) tensors / (B, H, n) row vectors that
     may be views of rows of longer sequences (0 when packed); raises for other layouts."""
@@ -404,11 +433,9 @@ def forward(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, 
     sinks = _sinks(sinks)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
     _packed("forward", q, k, v, out, lse)
+    out, lse = _fill(stream, (out, lambda: torch.empty_like(q)),
+                     (lse, lambda: torch.empty((B, H, n), dtype=torch.float32, device=q.device)))
     _shaped("forward", [(out, q.shape, q.dtype), (lse, (B, H, n) if q.dim() == 4 else (n,),
                                                   torch.float32)])
     if sinks:
@@ -461,9 +488,6 @@ def backward(q, k, v, o, do, lse, causal=False, scale=None, deterministic=False,
     Hkv, nk = _kv_heads(q, k, v)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
     sinks = _sinks(sinks)
     if sinks:
         wl, wr = _window(causal, window)
@@ -471,9 +495,13 @@ def backward(q, k, v, o, do, lse, causal=False, scale=None, deterministic=False,
                                              int(bool(deterministic)))
     else:
         need = attn_bwd_workspace_bytes(B, H, n, d, int(bool(deterministic)))
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is not None and workspace.numel() * workspace.element_size() < need:
+        workspace = None
     _packed("backward", q, k, v, o, do, lse, dq, dk, dv, workspace)
+    dq, dk, dv, workspace = _fill(
+        stream, (dq, lambda: torch.empty_like(q)), (dk, lambda: torch.empty_like(k)),
+        (dv, lambda: torch.empty_like(v)),
+        (workspace, lambda: torch.empty(need, dtype=torch.uint8, device=q.device)))
     lse_shape = (B, H, n) if q.dim() == 4 else (n,)
     _shaped("backward", [(o, q.shape, q.dtype), (do, q.shape, q.dtype),
                          (lse, lse_shape, torch.float32), (dq, q.shape, q.dtype),
@@ -515,8 +543,15 @@ class BackwardSum:
         self.B, self.H, self.n, self.d = _dims(o)
         self.det = int(bool(deterministic))
         need = attn_bwd_workspace_bytes(self.B, self.H, self.n, self.d, self.det)
-        self.ws = torch.empty(need, dtype=torch.uint8, device=o.device)
+        _packed("BackwardSum", o, do, lse)
+        self.ws, = _fill(stream, (None, lambda: torch.empty(need, dtype=torch.uint8, device=o.device)))
         self.reset(o, do, lse, stream)
+
+    def _run_on(self, stream):
+        """The stream's handle; the workspace is not reused before the stream is done with it."""
+        import torch
+        self.ws.record_stream(torch.cuda.current_stream() if stream is None else _torch_stream(stream))
+        return _stream_handle(stream)
 
     def reset(self, o, do, lse, stream=None):
         import torch
@@ -526,7 +561,7 @@ class BackwardSum:
         _shaped("BackwardSum", [(do, o.shape, o.dtype), (lse, o.shape[:-1], torch.float32)])
         rc = attn_bwd_prepare(_ptr(o), _ptr(do), _ptr(lse), self.B, self.H, self.n, self.d,
                               _dtype_code(o), self.det, _ptr(self.ws), self.ws.numel(),
-                              _stream_handle(stream))
+                              self._run_on(stream))
         _check(rc, "attn_bwd_prepare")
 
     def add(self, q, k, v, do, dk_acc, dv_acc, scale=None, causal=False, window=None,
@@ -552,22 +587,21 @@ class BackwardSum:
         rc = attn_bwd_accumulate(_ptr(q), _ptr(k), _ptr(v), _ptr(do), _ptr(dk_acc), _ptr(dv_acc),
                                  self.B, self.H, Hkv, nq, nk, self.d, q_rows, kv_rows, self.n,
                                  int(q_row0), float(scale), wl, wr, _dtype_code(q), self.det,
-                                 _ptr(self.ws), self.ws.numel(), _stream_handle(stream))
+                                 _ptr(self.ws), self.ws.numel(), self._run_on(stream))
         _check(rc, "attn_bwd_accumulate")
 
     def finish(self, dq=None, scale=None, stream=None):
         """dQ (bf16, (B, H, n, d)) = scale · the dQ sum."""
         import torch
-        if dq is None:
-            dq = torch.empty((self.B, self.H, self.n, self.d), dtype=torch.bfloat16,
-                             device=self.ws.device)
+        dq, = _fill(stream, (dq, lambda: torch.empty((self.B, self.H, self.n, self.d),
+                                                     dtype=torch.bfloat16, device=self.ws.device)))
         if scale is None:
             scale = 1.0 / math.sqrt(self.d)
         _packed("BackwardSum.finish", dq, self.ws)
         _shaped("BackwardSum.finish", [(dq, (self.B, self.H, self.n, self.d), torch.bfloat16)])
         rc = attn_bwd_finish(_ptr(dq), self.B, self.H, self.n, self.d, float(scale),
                              _dtype_code(dq), self.det, _ptr(self.ws), self.ws.numel(),
-                             _stream_handle(stream))
+                             self._run_on(stream))
         _check(rc, "attn_bwd_finish")
         return dq
 
@@ -628,11 +662,9 @@ def forward_fp8(q, k, v, q_descale=1.0, k_descale=1.0, v_descale=1.0, causal=Fal
     sinks = _sinks(sinks)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
     _packed("forward_fp8", q, k, v, out, lse)
+    out, lse = _fill(stream, (out, lambda: torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)),
+                     (lse, lambda: torch.empty((B, H, n), dtype=torch.float32, device=q.device)))
     _shaped("forward_fp8", [(out, q.shape, torch.bfloat16),
                             (lse, (B, H, n) if q.dim() == 4 else (n,), torch.float32)])
     wl, wr = _window(causal, window)

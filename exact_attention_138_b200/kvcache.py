@@ -24,7 +24,7 @@ import math
 
 import torch
 
-from . import AttnError, _lib, _sinks
+from . import AttnError, _fill, _lib, _sinks, _torch_stream
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _lib.attn_kv4_page_bytes.restype = _sz
@@ -131,12 +131,12 @@ def _is(where, name, t, dtype, *shape):
     raise ValueError(f"{where}: {name} must be {dtype} {shape}, got {t.dtype} {tuple(have)}")
 
 
-def _raw_stream(stream, dev, *made):
-    """The stream's handle; tensors made here on the current stream are kept until `stream` is done."""
+def _raw_stream(stream, dev, *written):
+    """The stream's handle; what the call writes is not reused before `stream` is done with it."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
-    for t in made:
-        t.record_stream(stream)
+    for t in written:
+        t.record_stream(_torch_stream(stream))
     return stream.cuda_stream
 
 
@@ -206,14 +206,11 @@ def kv4_gather(pool, table, start, n, d, counts=None, seqs=None, k=None, v=None,
         raise ValueError(f"{where}: n must be 1 or more")
     dev = _tensors(where, pool, table, start, counts, seqs, k, v)
     shape = (B, pool.shape[1], n, d)
-    if k is None:
-        k = pool.new_empty(shape, dtype=torch.bfloat16)
-    else:
-        _is(where, "k", k, torch.bfloat16, *shape)
-    if v is None:
-        v = torch.empty_like(k)
-    else:
-        _is(where, "v", v, torch.bfloat16, *shape)
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _is(where, name, t, torch.bfloat16, *shape)
+    make = lambda: pool.new_empty(shape, dtype=torch.bfloat16)          # noqa: E731
+    k, v = _fill(stream, (k, make), (v, make))
     rc = _lib.attn_kv4_gather(pool.data_ptr(), table.data_ptr(), _at(seqs), start.data_ptr(),
                               _at(counts), k.data_ptr(), v.data_ptr(), pool.shape[0],
                               table.shape[0], table.shape[1], page, B, shape[1], n, d,
@@ -248,16 +245,13 @@ def kv4_attend(q, pool, table, lens, window=None, sinks=0, scale=None, seqs=None
     wl, wr = (-1, 0) if window is None else (int(window[0]), int(window[1]))
     sinks = _sinks(sinks)
     dev = _tensors(where, q, pool, table, lens, seqs, out, lse, workspace)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
+    if out is not None:
         _is(where, "out", out, torch.bfloat16, B, H, nq, d)
-    if lse is None:
-        lse = q.new_empty((B, H, nq), dtype=torch.float32)
-    else:
+    if lse is not None:
         _is(where, "lse", lse, torch.float32, B, H, nq)
-    if workspace is None:
-        workspace = pool.new_empty(_lib.attn_kv4_workspace_bytes(H, Hkv, nq, d))
+    out, lse, workspace = _fill(
+        stream, (out, lambda: torch.empty_like(q)), (lse, lambda: q.new_empty((B, H, nq), dtype=torch.float32)),
+        (workspace, lambda: pool.new_empty(_lib.attn_kv4_workspace_bytes(H, Hkv, nq, d))))
     rc = _lib.attn_kv4_attend(q.data_ptr(), pool.data_ptr(), table.data_ptr(), _at(seqs),
                               lens.data_ptr(), out.data_ptr(), lse.data_ptr(), pages, slots, width,
                               page, B, H, Hkv, nq, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
@@ -289,7 +283,7 @@ def pages_reserve(table, lens, refs, page_size, seqs, counts, stream=None):
     refused: pages or table columns ran out, or a row is out of range or given twice."""
     where = "pages_reserve"
     pages, slots, width, dev = _page_state(where, table, lens, refs, seqs, counts)
-    start = torch.empty_like(seqs)
+    start, = _fill(stream, (None, lambda: torch.empty_like(seqs)))
     rc = _lib.attn_pages_reserve(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), seqs.data_ptr(),
                                  counts.data_ptr(), start.data_ptr(), pages, slots, width, page_size,
                                  seqs.shape[0], _raw_stream(stream, dev, start))
@@ -304,7 +298,7 @@ def pages_fork(table, lens, refs, page_size, src, dst, stream=None):
     or the call was refused (pages ran out, a dst not empty, given twice or also a src)."""
     where = "pages_fork"
     pages, slots, width, dev = _page_state(where, table, lens, refs, src, dst)
-    frm, to = torch.empty_like(src), torch.empty_like(src)
+    frm, to = _fill(stream, *[(None, lambda: torch.empty_like(src))] * 2)
     rc = _lib.attn_pages_fork(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), src.data_ptr(),
                               dst.data_ptr(), frm.data_ptr(), to.data_ptr(), pages, slots, width, page_size,
                               src.shape[0], _raw_stream(stream, dev, frm, to))
@@ -338,10 +332,10 @@ def pages_compact(table, refs, workspace=None, stream=None):
     if workspace is not None:
         _tensors(where, workspace)
     need = (pages + 4) * 4
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=refs.device)
     half = max(pages // 2, 1)
-    out = torch.empty(2 * half + 1, dtype=torch.int32, device=refs.device)
+    out, workspace = _fill(
+        stream, (None, lambda: torch.empty(2 * half + 1, dtype=torch.int32, device=refs.device)),
+        (workspace, lambda: torch.empty(need, dtype=torch.uint8, device=refs.device)))
     frm, to, count = out[:half], out[half:2 * half], out[2 * half:]
     rc = _lib.attn_pages_compact(table.data_ptr(), refs.data_ptr(), frm.data_ptr(), to.data_ptr(),
                                  count.data_ptr(), pages, slots, width, workspace.data_ptr(),
