@@ -626,10 +626,10 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
         if (in_sinks && f_li >= f_sb) place();
     };
     uint32_t valid = 0;                    // BL bits per stage: blocks on a page
-    int issued = 0, taken = 0, fs = 0, cs = 0;             // steps, and their stages
-    uint32_t phase = 0;
+    Kv4Ring<ST> steps;
     auto fetch = [&]() {
         if (!more) return;
+        const int fs = steps.fill;
         const bool held = static_cast<unsigned>(pid) < static_cast<unsigned>(a.pool.pages);
         const uint32_t bits = __ballot_sync(0xffffffffu, held);
         valid = (valid & ~(((1u << C::BL) - 1u) << (fs * C::BL))) | bits << (fs * C::BL);
@@ -639,15 +639,13 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
             bulk_load(ring + fs * C::SB + lane * C::BB,
                       heads + static_cast<size_t>(pid) * page_bytes + static_cast<size_t>(n_blk) * C::BB, C::BB,
                       &full[fs]);
-        ++issued;
-        fs = fs + 1 == ST ? 0 : fs + 1;
+        steps.start();
         look();
     };
     open();
     look();
     for (int s = 0; s < ST; ++s) fetch();
 
-    bool ok = true;
     while (true) {
         // ---- one segment's part of the run
         const int head = q.hr / p.RB, row0 = q.hr % p.RB * C::ROWS;
@@ -987,9 +985,8 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
         const int sb = q.seq.sb, wb0 = q.seq.wb0 - sb;
         int li = q.t0 * C::TILE + warp * C::BL;
         for (int i = 0; i < mine; ++i, li += C::TILE) {
-            ok = bounded_wait_warp(&full[cs], phase, abort, lim);
-            ++taken;
-            if (!ok) break;
+            const int cs = steps.use;
+            if (!bounded_wait_warp(&full[cs], steps.phase, abort, lim)) break;
             const uint32_t on = valid >> (cs * C::BL) & ((1u << C::BL) - 1u);
             if (on) {
                 int tb[C::BL];
@@ -1003,10 +1000,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
                 if (inner) step(blk, tb, on, std::false_type{});
                 else step(blk, tb, on, std::true_type{});
             }
-            if (++cs == ST) {
-                cs = 0;
-                phase ^= 1u;
-            }
+            steps.take();
             __syncwarp();           // every lane has read the stage
             fetch();
         }
@@ -1109,10 +1103,10 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NT>::CTAS) kv4_attend_k
         }
         if (!more_parts) break;
     }
-    if (!ok || *abort) {          // let the copies in flight land
+    if (*abort) {                 // let the copies in flight land
         const uint64_t t0 = globaltimer_ns();
-        for (int i = taken > 0 ? taken - 1 : 0; i < issued; ++i)
-            while (!mbar_try_wait(&full[i % ST], (i / ST) & 1))
+        for (; steps.taken < steps.issued; steps.take())
+            while (!mbar_try_wait(&full[steps.use], steps.phase))
                 if (globaltimer_ns() - t0 > 100000000ull) break;
     }
 }

@@ -53,6 +53,27 @@ struct Kv4AttendArgs {
     uint64_t timeout_ns;
 };
 
+// One warp's ring of `ST` stages in the cache's attention: steps [0, issued) were started, [0, taken) waited
+// for and used. A wait that runs out changes nothing here, so that the steps [taken, issued) are always the
+// copies that may still be on their way.
+template <int ST>
+struct Kv4Ring {
+    int issued = 0, taken = 0;
+    int fill = 0, use = 0;         // stages of steps `issued` and `taken`
+    uint32_t phase = 0;            // of step `taken`
+    __host__ __device__ void start() {
+        ++issued;
+        fill = fill + 1 == ST ? 0 : fill + 1;
+    }
+    __host__ __device__ void take() {
+        ++taken;
+        if (++use == ST) {
+            use = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 cudaError_t launch_kv4_append(const Kv4RowsArgs& a, cudaStream_t stream);
 cudaError_t launch_kv4_gather(const Kv4RowsArgs& a, cudaStream_t stream);
 cudaError_t launch_kv4_attend(const Kv4AttendArgs& a, cudaStream_t stream);
