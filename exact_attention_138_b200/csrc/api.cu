@@ -617,7 +617,7 @@ static int check_pages(PageState& s, int* table, int* lens, int* refs, int pages
                        int max_pages, int page_size) {
     if (!table || !lens || !refs || !aligned4(table) || !aligned4(lens) || !aligned16(refs))
         return ATTN_ERR_INVALID;
-    if (pages < 1 || pages > kMaxSeq || slots < 1 || slots > kPagesMaxSlots || max_pages < 1 ||
+    if (pages < 1 || pages > kPagesMaxPages || slots < 1 || slots > kPagesMaxSlots || max_pages < 1 ||
         page_size < 1 || static_cast<long long>(max_pages) * page_size > kMaxSeq)
         return ATTN_ERR_INVALID;
     s = PageState{table, lens, refs, pages, slots, max_pages, page_size};

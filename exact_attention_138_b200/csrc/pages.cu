@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kPgThreads = 1024, kPgWarps = kPgThreads / 32;
 constexpr int kPgTile = 4 * kPgThreads;       // pages one CTA looks at per step, 4 per thread
+static_assert(kPagesMaxPages <= 0x7fffffff - 2 * kPgTile, "scan indices");
 constexpr int kPgCluster = 8;
 constexpr int kErrPages = 6;                  // ATTN_ERR_PAGES
 

@@ -16,6 +16,8 @@ struct PageState {
 
 constexpr int kPagesMaxSeqs = 8192;           // sequences per reserve / fork call
 constexpr int kPagesMaxSlots = 1 << 18;       // table rows (a bitmap of them lies in shared memory)
+constexpr int kPagesMaxPages = 0x7fffffff - 8192;   // the scans' 32-bit indices pass the last page by up to
+                                                    // a tile (4096 pages)
 
 cudaError_t launch_pages_reserve(const PageState& s, const int* seqs, const int* counts, int* start,
                                  int n, cudaStream_t stream);

@@ -395,8 +395,9 @@ int attn_kv4_attend(const void* q, const void* pool, const int* table, const int
  * attn_pages_copy: contents of page from[i] to page to[i], i < min(n, *count) (count NULL: n), in each
  *   of `layers` pools of `pages` pages of page_bytes bytes that follow one another. Pairs with a number
  *   outside [0, pages) are skipped; no page may be both copied from and to.
- * n <= 8192 sequences for reserve and fork, slots <= 262144; other sizes below 1, null or misaligned
- * pointers, max_pages·page_size > 2^31 - 257, page_bytes no multiple of 16 -> ATTN_ERR_INVALID. */
+ * n <= 8192 sequences for reserve and fork, slots <= 262144, pages < 2^31 - 8192 (all but copy); other sizes
+ * below 1, null or misaligned pointers, max_pages·page_size > 2^31 - 257, page_bytes no multiple of 16 ->
+ * ATTN_ERR_INVALID. */
 int attn_pages_reserve(int* table, int* lens, int* refs, const int* seqs, const int* counts,
                        int* start, int pages, int slots, int max_pages, int page_size, int n,
                        void* stream);
