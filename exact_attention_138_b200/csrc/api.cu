@@ -526,8 +526,7 @@ static int check_pool(Kv4Pool& p, const void* pool, const int* table, const int*
     if (!pool || !table) return ATTN_ERR_INVALID;
     if (!aligned16(pool) || !aligned4(table) || !aligned4(seqs)) return ATTN_ERR_INVALID;
     if (d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
-    if (page_size < kKv4Block || page_size % kKv4Block != 0 || page_size > 65536)
-        return ATTN_ERR_INVALID;
+    if (page_size < kKv4Block || page_size % kKv4Block != 0) return ATTN_ERR_INVALID;
     if (pages < 1 || slots < 1 || max_pages < 1 || B < 1 || B > 65535 || Hkv < 1 || Hkv > 65535)
         return ATTN_ERR_INVALID;
     if (static_cast<long long>(max_pages) * page_size > kMaxSeq) return ATTN_ERR_INVALID;
