@@ -393,12 +393,11 @@ def _kv_heads(q, k, v):
 
 def _window(causal, window):
     """(window_left, window_right): None -> causal (-1, 0) or none (-1, -1); causal=True with a
-    window caps the right side at 0. Negative = unbounded."""
+    window caps the right side at 0. Negative = unbounded, and so is a bound beyond 32 bits, which
+    lies further than any key."""
     if window is None:
         return (-1, 0) if causal else (-1, -1)
-    wl, wr = (int(window[0]), int(window[1]))
-    wl = -1 if wl < 0 else wl
-    wr = -1 if wr < 0 else wr
+    wl, wr = (x if 0 <= x <= 0x7fffffff else -1 for x in (int(window[0]), int(window[1])))
     if causal:
         wr = 0
     return wl, wr

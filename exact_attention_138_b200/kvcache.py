@@ -24,7 +24,7 @@ import math
 
 import torch
 
-from . import AttnError, _fill, _lib, _sinks, _torch_stream
+from . import AttnError, _fill, _lib, _sinks, _torch_stream, _window
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _lib.attn_kv4_page_bytes.restype = _sz
@@ -200,6 +200,8 @@ def kv4_gather(pool, table, start, n, d, counts=None, seqs=None, k=None, v=None,
     bf16: k, v (B, kv_heads, n, d). Rows at or beyond counts[i], of entries with a negative start and
     on no page are zeros."""
     where = "kv4_gather"
+    if start.dim() != 1:
+        _is(where, "start", start, torch.int32, None)
     B = start.shape[0]
     page = _rows(where, pool, table, d, B, start, counts, seqs)
     if n < 1:
@@ -233,7 +235,7 @@ def kv4_attend(q, pool, table, lens, window=None, sinks=0, scale=None, seqs=None
     B, H, nq, d = q.shape
     page = _page_size(where, pool, d)
     pages, Hkv, _ = pool.shape
-    if H % Hkv:
+    if Hkv < 1 or H % Hkv:
         raise ValueError(f"{where}: H must be a multiple of the pool's K/V heads")
     if q.dtype is not torch.bfloat16 or table.dtype is not torch.int32 or table.dim() != 2:
         _is(where, "q", q, torch.bfloat16, B, H, nq, d)
@@ -242,7 +244,7 @@ def kv4_attend(q, pool, table, lens, window=None, sinks=0, scale=None, seqs=None
     _is(where, "lens", lens, torch.int32, slots)
     if seqs is not None:
         _is(where, "seqs", seqs, torch.int32, B)
-    wl, wr = (-1, 0) if window is None else (int(window[0]), int(window[1]))
+    wl, wr = _window(window is None, window)
     sinks = _sinks(sinks)
     dev = _tensors(where, q, pool, table, lens, seqs, out, lse, workspace)
     if out is not None:
@@ -273,7 +275,7 @@ def _page_state(where, table, lens, refs, *ts):
     if refs.dtype is not torch.int32 or refs.dim() != 1:
         _is(where, "refs", refs, torch.int32, None)
     for t in ts:
-        _is(where, "rows and counts", t, torch.int32, ts[0].shape[0])
+        _is(where, "rows and counts", t, torch.int32, ts[0].shape[0] if ts[0].dim() else None)
     return refs.shape[0], slots, width, _tensors(where, table, lens, refs, *ts)
 
 
@@ -314,7 +316,7 @@ def pages_free(table, lens, refs, page_size, seqs, window=None, sinks=0, stream=
     where = "pages_free"
     pages, slots, width, dev = _page_state(where, table, lens, refs, seqs)
     sinks = _sinks(sinks)
-    left = -1 if window is None else int(window[0])
+    left = _window(False, window)[0]
     if window is not None and left < 0:
         return                                  # an open window: every token stays visible
     rc = _lib.attn_pages_free(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), seqs.data_ptr(), pages,
