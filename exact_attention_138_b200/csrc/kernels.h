@@ -159,7 +159,7 @@ struct BwdArgs {
     int ws_rows = 0, q_row0 = 0;
     // Sinks (see MaskSpec): the queries of each key tile that holds one are shared by sink_parts
     // CTAs; if there are several, their dK, dV partials (B·Hkv, sink tiles, parts, 128 rows, d fp32; all
-    // dK, then all dV) lie in sink_buf and are summed in a launch of their own.
+    // dK, then all dV) lie in sink_buf and are summed in the launch that converts dQ.
     int ns = 0, sink_parts = 0;
     float* sink_buf = nullptr;
 };

@@ -3,9 +3,10 @@
 // that admits, forks and ends sequences needs no read-back and can be captured into a graph.
 //
 // Results depend on the state alone, not on timing: free pages are handed out from the lowest number up
-// in the order of the requests, and reference counts change by integer atomics. A call that cannot be
-// served (too few free pages, an index out of range or given twice, no room in the table) changes
-// nothing, marks its results with -1 and sets the device status.
+// in the order of the requests, and reference counts change by integer atomics. A reserve or fork that
+// cannot be served (too few free pages, an index out of range or given twice, no room in the table)
+// changes nothing, marks its results with -1 and sets the device status; free passes over rows out of
+// range, serves the others and sets it too.
 //
 // What bounds them: the page copies by HBM; the others are a chain of a few dependent reads (sequence
 // -> length -> table entry -> count), so they are launched once, as one cluster of up to 8 CTAs that

@@ -15,7 +15,8 @@ Pages: with lens (slots,) and refs (pages,), int32 like the table and all of it 
     pages_free(table, lens, refs, page_size, seqs, window=(1024, 0), sinks=4)  # what no query sees
     pages_copy(pool, *pages_compact(table, refs))                         # pages in use come first
 
-A call that cannot be served changes nothing; `device_status()` then says ATTN_ERR_PAGES.
+A reserve or fork that cannot be served changes nothing, and pages_free passes over rows out of range;
+`device_status()` then says ATTN_ERR_PAGES.
 """
 from __future__ import annotations
 
@@ -312,7 +313,8 @@ def pages_fork(table, lens, refs, page_size, src, dst, stream=None):
 def pages_free(table, lens, refs, page_size, seqs, window=None, sinks=0, stream=None):
     """Without a window the sequences end: their pages lose a reference, their rows and lengths are
     cleared. With window=(left, right) only pages are given back whose tokens no query from the next
-    token on sees under that window and these sinks; their entries become -1."""
+    token on sees under that window and these sinks; their entries become -1. Rows out of range are passed
+    over (and reported by `device_status()`), the others served."""
     where = "pages_free"
     pages, slots, width, dev = _page_state(where, table, lens, refs, seqs)
     sinks = _sinks(sinks)

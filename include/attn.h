@@ -40,7 +40,8 @@
  *                      limit and the kernel returned early (outputs are then undefined);
  *   ATTN_ERR_PAGES     reported by attn_get_device_status(): an attn_pages_* call was refused on the
  *                      device (too few free pages, an index out of range or given twice) and
- *                      changed nothing.
+ *                      changed nothing; or attn_pages_free passed over a row out of range and
+ *                      served the others.
  */
 #ifndef ATTN_H
 #define ATTN_H
@@ -375,8 +376,8 @@ int attn_kv4_attend(const void* q, const void* pool, const int* table, const int
  * lens 0 and a row of -1. The state is read and changed on the device, in stream order, without
  * synchronising; calls on one state must be ordered. Contents move only by attn_pages_copy, once for
  * every pool that the table serves. Free pages are taken from the lowest number up, in the order of
- * the entries. A call that cannot be served as a whole changes nothing: start, from and to are -1 and
- * the device status becomes ATTN_ERR_PAGES.
+ * the entries. A reserve or fork that cannot be served as a whole changes nothing: start, from and to
+ * are -1 and the device status becomes ATTN_ERR_PAGES.
  *
  * attn_pages_reserve: sequences seqs[i] grow by counts[i] >= 0 tokens; start[i] = its length before, the
  *   first new token (for attn_kv4_append, which leaves out entries with a negative start). Refused
@@ -387,8 +388,8 @@ int attn_kv4_attend(const void* q, const void* pool, const int* table, const int
  *   empty, given twice or also a src, or a row is out of range.
  * attn_pages_free: window_left < 0: the sequences end (lens 0, row -1). window_left >= 0: only pages
  *   whose tokens no query from the next token on sees under that window and n_sink sinks are given
- *   back; their entries become -1. Rows out of range are skipped (and reported); a row given twice
- *   counts once. n >= 1 rows.
+ *   back; their entries become -1. Rows out of range are passed over, with ATTN_ERR_PAGES in the device
+ *   status, and the others served; a row given twice counts once. n >= 1 rows.
  * attn_pages_compact: the L pages in use move to the numbers below L: from[r] -> to[r] for r < *count,
  *   both ascending, -1 behind; from and to hold max(pages / 2, 1) entries. Table and refs follow.
  *   Workspace: attn_pages_workspace_bytes(pages), 16-byte aligned.

@@ -1,5 +1,6 @@
 """The device status: a refused page call, which a full cache meets in ordinary use, neither hides a fault
-that a kernel reports after it nor is lost behind one that was reported before it."""
+that a kernel reports after it nor is lost behind one that was reported before it. Freeing rows out of range,
+which is reported in the same way, serves the others."""
 import pytest
 import torch
 
@@ -38,3 +39,15 @@ def test_each_alone_is_reported_once(cuda_device, what, code):
     ea.device_status()
     what()
     assert [ea.device_status() for _ in range(2)] == [code, ea.ATTN_OK]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [None, (0, 0)])
+def test_freeing_passes_over_rows_out_of_range_and_reports_them(cuda_device, window):
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")     # noqa: E731
+    table, lens, refs = i32([[0, 1], [2, -1], [3, -1]]), i32([32, 16, 16]), i32([1, 1, 1, 1, 0])
+    ea.device_status()
+    ea.pages_free(table, lens, refs, 16, i32([0, 3, 1, -1]), window=window)
+    assert ea.device_status() == ea.ATTN_ERR_PAGES and ea.device_status() == ea.ATTN_OK
+    assert table.tolist() == [[-1, -1], [-1, -1], [3, -1]] and refs.tolist() == [0, 0, 0, 1, 0]
+    assert lens.tolist() == ([0, 0, 16] if window is None else [32, 16, 16])
