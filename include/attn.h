@@ -161,6 +161,8 @@ int attn_fwd_ex(const void* q, const void* k, const void* v, void* o, float* lse
  *     j <= i + off + window_right   and   (j >= i + off - window_left  or  j < n_sink);
  * a negative bound is none, so n_sink changes nothing when window_left is negative, and n_sink = 0
  * is attn_fwd_ex; n_sink >= nk leaves no left bound. bf16 and fp32; one launch, no library memory.
+ * As in every forward and backward here, a key that a query does not see has the weight 0 in the products
+ * of its tile of 128 keys: V (and K in the backward) must be finite there, since 0 times a NaN is NaN.
  * Errors as attn_fwd_ex; n_sink < 0 is ATTN_ERR_INVALID. */
 int attn_fwd_sink(const void* q, const void* k, const void* v, void* o, float* lse,
                   int B, int H, int Hkv, int nq, int nk, int d, float scale,
