@@ -917,8 +917,9 @@ int max_active_clusters(int split, int sms, cudaStream_t stream) {
 }
 
 // Key shares per tile pair for the forward: 1 when the pairs alone fill half the SMs, else the
-// largest power of two (at most 8, at most the largest number of key tiles a query tile sees)
-// that keeps the grid within one CTA per SM and every cluster resident at once.
+// largest power of two (at most 8, at most the largest number of key tiles in a query tile's window;
+// sinks' tiles before it are not counted) that keeps the grid within one CTA per SM and every cluster
+// resident at once.
 template <int D, bool F8>
 int choose_fwd_split(const MaskSpec& mk, int qtiles, long long pairs_total, cudaStream_t stream) {
     int dev = 0, sms = 0;

@@ -157,3 +157,29 @@ def test_results_on_a_busy_stream(cuda_device, data, name):
     assert ea.device_status() in (ea.ATTN_OK, ea.ATTN_ERR_PAGES)
     for g, w in zip(got, want):
         assert torch.equal(g, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["forward, sinks", "backward, sinks", "kv4_attend", "kv4_gather", "BackwardSum"])
+def test_a_branch_of_a_captured_graph(cuda_device, data, name):
+    # the call runs on a stream that joins the capture, while the capturing stream makes memory of its own
+    flat = lambda r: list(r) if isinstance(r, (tuple, list)) else [r]        # noqa: E731
+    x = _fresh(data)
+    want = [t.clone() for t in flat(CALLS[name](x, None))]
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        got = flat(CALLS[name](x, side))
+        other = [torch.full_like(t, 3) for t in want for _ in range(3)]
+        main.wait_stream(side)
+        back = [t.clone() for t in got]
+        del got
+    for _ in range(2):
+        for t in back + other:
+            t.fill_(-1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(b, w) for b, w in zip(back, want))
+        assert all(bool((t == 3).all()) for t in other)
